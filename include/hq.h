@@ -510,6 +510,121 @@ hq_status hq_quant_mxfp4(const void* X, hq_dtype xt, int64_t M, int64_t K, int64
 hq_status hq_mxfp4_linear(const uint8_t* Xq, const uint8_t* sx, int64_t M, int64_t K, const uint8_t* Wq,
                           const uint8_t* sw, int64_t N, float* Y, int32_t accumulate, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Between two layers of a decoder: residual stream, gate and norms, alone or
+ * with the next layer's rotation and quantiser; low-rank adapters of many
+ * requests beside a layer.  All run on the caller's stream, need no host
+ * synchronisation and can be captured into a CUDA graph.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * hq_residual_norm -- the residual stream updated with a block's output and the
+ * norm the next layer reads.  Per row of K channels, in fp32, every product
+ * and sum rounded on its own, e() rounding to the type xt:
+ *   p = Y | fl(fl(Y * fl(w_post + w_offset)) * r(Y))   (w_post NULL | given)
+ *   p = fl(gate * p)                                   (gate given)
+ *   h = e(fl(H + fl(alpha * p)))                       (h = H when Y is NULL)
+ *   X = e(fl(fl(h * fl(w + w_offset)) * r(h)))         (w given)
+ * with r(v) = 1 / sqrt(sum v^2 / K + eps), the sum in fp32 (|v| below 1e18).
+ *  H        device, [M][ld_h] residual stream
+ *  Y        device, [M][ld_y] the block's output, or NULL (no block: H is normed)
+ *  xt       type of H, Y, gate, H_out and X: HQ_F16, HQ_BF16 or HQ_F32
+ *  w_post   device, [K] weights of the norm after the block, or NULL (none)
+ *  gate     device, [M][ld_gate] factors per token and channel; ld_gate = 0: one
+ *           row [K] for all tokens; NULL: none
+ *  alpha    residual scale
+ *  w        device, [K] weights of the next norm, or NULL (then X is NULL too and
+ *           only H_out is written)
+ *  wt       type of w and w_post (any of the three); w_offset is added to both
+ *           (1 for weights stored as their distance from one)
+ *  H_out    device, [M][ld_ho] h (output), or NULL;  may be H itself (same stride)
+ *  X        device, [M][ld_x] the normed rows (output);  may be Y itself (same stride)
+ * Any K up to 16384.  Pointers 16-byte aligned, strides multiples of 16 bytes.
+ * A row's outputs depend on that row alone (NaN and infinities stay in it).
+ * Errors: HQ_ERR_ARG (M < 0, K <= 0, a bad type, a stride below K, eps negative or
+ * NaN, gate or w_post without Y, w without X or X without w, no output, H NULL with
+ * M > 0), HQ_ERR_ALIGN, HQ_ERR_UNSUPPORTED (K > 16384, M above INT32_MAX),
+ * HQ_ERR_CUDA.  M == 0 is a no-op.
+ */
+hq_status hq_residual_norm(const void* H, int64_t ld_h, const void* Y, int64_t ld_y, hq_dtype xt, int64_t M, int64_t K,
+                           const void* w_post, const void* gate, int64_t ld_gate, float alpha, const void* w,
+                           hq_dtype wt, float w_offset, float eps, void* H_out, int64_t ld_ho, void* X, int64_t ld_x,
+                           void* stream);
+
+/*
+ * hq_norm_rotate_quant -- hq_residual_norm (without a norm after the block)
+ * followed by hq_rotate_quant / hq_rotate_quant8 in one pass.  A per-token
+ * symmetric quantiser does not see a factor common to the row, so the norm's
+ * r(h) goes into the scale only; with v = fl(h * fl(w + w_offset)) in fp32
+ *   u = (v .* d) * H_sylv            as hq_rotate_quant
+ *   q = clamp(rint(fl32(u * fl32(7/amax))), -7, 7),  amax = max |u| of the row
+ *   sx = fl32(fl32(fl32(amax/7) * fl32(1/sqrt(group))) * r(h))
+ * (127 in place of 7 for bits = 8): the codes depend on no sum over the row
+ * and skip the 16-bit rounding of the normed row that the two calls in
+ * sequence have.
+ *  H .. eps as hq_residual_norm, xt HQ_F16 or HQ_BF16;  Y, gate, H_out and X may be
+ *           NULL (X: the normed rows, for callers that need them as well)
+ *  group, H_signs   as hq_rotate_quant
+ *  bits     4: Xq device, [M][K/2] packed codes; 8: [M][K] int8 codes (output)
+ *  sx       device, [M] fp32 (output); NaN for a row that holds a NaN or infinity
+ * Errors: as hq_residual_norm and hq_rotate_quant; HQ_ERR_ARG for other bits.
+ */
+hq_status hq_norm_rotate_quant(const void* H, int64_t ld_h, const void* Y, int64_t ld_y, hq_dtype xt, int64_t M,
+                               int64_t K, const void* gate, int64_t ld_gate, float alpha, const void* w, hq_dtype wt,
+                               float w_offset, float eps, int32_t group, const int8_t* H_signs, int32_t bits,
+                               void* H_out, int64_t ld_ho, void* X, int64_t ld_x, void* Xq, float* sx, void* stream);
+
+/*
+ * hq_lora_plan -- the tokens of a batch grouped by adapter, once per batch for
+ * every adapted layer of the step.
+ *  ids    device, [M] int32: the token's adapter in [0, n), or -1 for none.
+ *         Another value counts as -1 and records HQ_ERR_ARG in the device
+ *         status word (hq_last_device_status).
+ *  order  device, [M] int32 (output): the tokens sorted by id, -1 first, those of
+ *         one id in their order
+ *  tiles  device, [hq_lora_max_tiles(M, n)][3] int32 (output): `order` cut into
+ *         runs of at most 64 tokens of one id: (id, first position, tokens), in
+ *         order; unused entries are (-1, 0, 0)
+ * Errors: HQ_ERR_ARG (M < 0, n < 0, NULL with M > 0), HQ_ERR_UNSUPPORTED (n > 1022,
+ * more than 65535 tiles), HQ_ERR_CUDA.  M == 0 is a no-op.
+ */
+int64_t hq_lora_max_tiles(int64_t M, int64_t n);
+hq_status hq_lora_plan(const int32_t* ids, int64_t M, int64_t n, int32_t* order, int32_t* tiles, void* stream);
+
+/*
+ * hq_lora_apply -- low-rank adapters beside a layer:
+ *   Y[m] = base[m] + scales[a] (X[m] A_a^T) B_a^T,  a = the token's adapter,
+ * over the adapter's own rank; Y[m] = base[m] for a token without one.  The
+ * inner product is summed and kept in fp32; Y is rounded once.
+ *  X        device, [M][ld_x] the layer's input (before rotation), HQ_F16 or HQ_BF16
+ *  A, B     device, [n][r_max][K] and [n][N][r_max], of X's type
+ *  r_max    a multiple of 8, up to 256
+ *  ranks    device, [n] int32 rank of each adapter in [0, r_max] (rows of A and
+ *           columns of B behind it are not used), or NULL: r_max for all.  A value
+ *           outside is clamped and records HQ_ERR_ARG in the device status word.
+ *  scales   device, [n] fp32, or NULL: 1
+ *  order, tiles   the hq_lora_plan outputs for the batch's ids and the same n.
+ *           Entries outside the batch are never read through; they record
+ *           HQ_ERR_ARG in the device status word.
+ *  base     device, [M][ld_b] of type yt (the layer's output), or NULL: zero.  May
+ *           be Y itself (same stride).
+ *  Y        device, [M][ld_y] of type yt: HQ_F16, HQ_BF16 or HQ_F32 (output)
+ *  workspace, ws_bytes   device scratch of hq_lora_workspace_size(M, r_max) bytes,
+ *           in use until the call's work on the stream is done
+ * Requirements: K % 8 == 0, N % 8 == 0; X, A, B, base, Y and workspace 16-byte
+ * aligned, row strides multiples of 16 bytes (HQ_ERR_ALIGN).
+ * Errors: HQ_ERR_ARG (sizes, types, strides, NULLs, a workspace too small, base
+ * equal to Y with another stride), HQ_ERR_ALIGN, HQ_ERR_UNSUPPORTED (the limits
+ * above, fp32 X), HQ_ERR_CUDA.  M == 0 or N == 0 is a no-op.
+ */
+size_t hq_lora_workspace_size(int64_t M, int32_t r_max);
+hq_status hq_lora_apply(const void* X, hq_dtype xt, int64_t M, int64_t K, int64_t ld_x, const void* A, const void* B,
+                        int64_t N, int64_t n, int32_t r_max, const int32_t* ranks, const float* scales,
+                        const int32_t* order, const int32_t* tiles, const void* base, int64_t ld_b, void* Y,
+                        hq_dtype yt, int64_t ld_y, void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

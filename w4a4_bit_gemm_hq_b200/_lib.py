@@ -64,6 +64,15 @@ SIGNATURES = {
     "hq_permute_channels": ([_P, ct.c_int, _I64, _I64, _I64, _P, _P, _I32, _P, _P], _ST),
     "hq_quant_mxfp4": ([_P, ct.c_int, _I64, _I64, _I64, _P, _P, _P], _ST),
     "hq_mxfp4_linear": ([_P, _P, _I64, _I64, _P, _P, _I64, _P, _I32, _P], _ST),
+    "hq_residual_norm": ([_P, _I64, _P, _I64, ct.c_int, _I64, _I64, _P, _P, _I64, ct.c_float, _P, ct.c_int,
+                          ct.c_float, ct.c_float, _P, _I64, _P, _I64, _P], _ST),
+    "hq_norm_rotate_quant": ([_P, _I64, _P, _I64, ct.c_int, _I64, _I64, _P, _I64, ct.c_float, _P, ct.c_int,
+                              ct.c_float, ct.c_float, _I32, _P, _I32, _P, _I64, _P, _I64, _P, _P, _P], _ST),
+    "hq_lora_max_tiles": ([_I64, _I64], _I64),
+    "hq_lora_plan": ([_P, _I64, _I64, _P, _P, _P], _ST),
+    "hq_lora_workspace_size": ([_I64, _I32], ct.c_size_t),
+    "hq_lora_apply": ([_P, ct.c_int, _I64, _I64, _I64, _P, _P, _I64, _I64, _I32, _P, _P, _P, _P, _P, _I64, _P,
+                       ct.c_int, _I64, _P, ct.c_size_t, _P], _ST),
     "hq_last_device_status": ([_P], _ST),
     "hq_debug_wait_probe": ([ct.c_uint64, _P], _ST),
 }

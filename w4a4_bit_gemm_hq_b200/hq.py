@@ -23,7 +23,8 @@ __all__ = [
     "hq_rotate_quant8", "w4a8_linear", "hq_debug_accum8", "hq_rotate_quant_asym", "w4a4_linear_asym",
     "hq_debug_accum_asym", "hq_calib_extreme_tokens", "hq_calib_top1_pca", "hq_calib_householder",
     "hq_calib_channel_absmax", "hq_calib_sorted_perm", "hq_calib_flatten_scales", "hq_permute_channels",
-    "calibrate_rotation_and_grouping", "hq_quant_mxfp4", "hq_mxfp4_linear",
+    "calibrate_rotation_and_grouping", "hq_quant_mxfp4", "hq_mxfp4_linear", "hq_residual_norm",
+    "hq_norm_rotate_quant", "hq_lora_max_tiles", "hq_lora_plan", "hq_lora_workspace_size", "hq_lora_apply",
 ]
 
 
@@ -355,6 +356,162 @@ def hq_mxfp4_linear(Xq, sx, Wq, sw, Y=None, accumulate=False):
     return Y
 
 
+# ------------------------------------------------- between two layers of a decoder
+# These calls check devices, types and shapes themselves (ValueError) and run
+# on the device of their first tensor, on its current stream.
+
+def _rows(t, name, like, M, K, dtype=None):
+    """Row stride in elements of an [M, K] tensor whose rows are contiguous."""
+    if t.device != like.device or not t.is_cuda:
+        raise ValueError("%s must be on the CUDA device of the first argument" % name)
+    if t.dtype != (like.dtype if dtype is None else dtype):
+        raise ValueError("%s must be %s, not %s" % (name, like.dtype if dtype is None else dtype, t.dtype))
+    if t.shape != (M, K):
+        raise ValueError("%s must have the shape (%d, %d), not %s" % (name, M, K, tuple(t.shape)))
+    if K > 1 and M > 0 and t.stride(1) != 1:
+        raise ValueError("%s must have contiguous rows" % name)
+    # the stride of a single row (or of none) says nothing
+    return t.stride(0) if M > 1 else max(K + 7 & ~7, t.stride(0) & ~7)
+
+
+def _vector(t, name, like, n, dtype):
+    if t.device != like.device or t.dtype != dtype or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of %d entries on the device of the first argument"
+                         % (name, dtype, n))
+
+
+def _whole(t, name, like, shape, dtype):
+    if t.device != like.device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on the device of the first argument"
+                         % (name, dtype, tuple(shape)))
+
+
+def _norm_args(H, w, Y, w_post, gate, H_out, X, M, K):
+    """Checks shared by the two calls below; the row strides (H, Y, gate, H_out, X) and the weights' type."""
+    wt = w.dtype if w is not None else w_post.dtype if w_post is not None else H.dtype
+    for t, name in ((w, "w"), (w_post, "w_post")):
+        if t is not None:
+            _vector(t, name, H, K, wt)
+    ld_g = 0
+    if gate is not None:
+        if gate.dim() == 1:
+            _vector(gate, "gate", H, K, H.dtype)
+        else:
+            ld_g = _rows(gate, "gate", H, M, K)
+    return (_rows(H, "H", H, M, K), 0 if Y is None else _rows(Y, "Y", H, M, K), ld_g,
+            0 if H_out is None else _rows(H_out, "H_out", H, M, K), 0 if X is None else _rows(X, "X", H, M, K), wt)
+
+
+def _new_rows(like, M, K):
+    """Empty [M, K] rows that start on 16 bytes."""
+    per = 16 // like.element_size()
+    pad = -(-K // per) * per
+    t = torch.empty((M, pad), dtype=like.dtype, device=like.device)
+    return t if pad == K else t[:, :K]
+
+
+def hq_residual_norm(H, w, eps, Y=None, w_post=None, gate=None, alpha=1.0, w_offset=0.0, H_out=None, X=None):
+    """(H_out, X): the residual stream H [M, K] plus alpha * gate * (norm of) the
+    block's output Y, and its RMS norm with weights w (None: no second norm, X is
+    None).  gate is [K] or [M, K]; w_offset is added to w and w_post.  H_out may
+    be H (in place) and X may be Y; without Y there is no H_out unless one is given."""
+    M, K = H.shape
+    if Y is not None and H_out is None:
+        H_out = _new_rows(H, M, K)
+    if w is not None and X is None:
+        X = _new_rows(H, M, K)
+    ld_h, ld_y, ld_g, ld_ho, ld_x, wt = _norm_args(H, w, Y, w_post, gate, H_out, X, M, K)
+    with torch.cuda.device(H.device):
+        check(lib.hq_residual_norm(ptr(H), ld_h, ptr(Y), ld_y, dtype_code(H.dtype), M, K, ptr(w_post), ptr(gate), ld_g,
+                                   alpha, ptr(w), dtype_code(wt), w_offset, eps, ptr(H_out), ld_ho, ptr(X), ld_x,
+                                   stream_handle()), "hq_residual_norm")
+    return H_out, X
+
+
+def hq_norm_rotate_quant(H, w, eps, group, H_signs=None, Y=None, gate=None, alpha=1.0, w_offset=0.0, bits=4,
+                         H_out=None, X=None, Xq=None, sx=None, want_x=False):
+    """(Xq, sx, H_out, X): hq_residual_norm (no norm after the block) with
+    hq_rotate_quant (bits=4) or hq_rotate_quant8 (bits=8) in one pass; the
+    normed rows X only with want_x or an X to write."""
+    M, K = H.shape
+    if Y is not None and H_out is None:
+        H_out = _new_rows(H, M, K)
+    if want_x and X is None:
+        X = _new_rows(H, M, K)
+    shape, dtype = ((M, K), torch.int8) if bits == 8 else ((M, K // 2), torch.uint8)
+    Xq = torch.empty(shape, dtype=dtype, device=H.device) if Xq is None else Xq
+    sx = torch.empty((M,), dtype=torch.float32, device=H.device) if sx is None else sx
+    _whole(Xq, "Xq", H, shape, dtype)
+    _vector(sx, "sx", H, M, torch.float32)
+    if H_signs is not None:
+        _vector(H_signs, "H_signs", H, group, torch.int8)
+    ld_h, ld_y, ld_g, ld_ho, ld_x, wt = _norm_args(H, w, Y, None, gate, H_out, X, M, K)
+    with torch.cuda.device(H.device):
+        check(lib.hq_norm_rotate_quant(ptr(H), ld_h, ptr(Y), ld_y, dtype_code(H.dtype), M, K, ptr(gate), ld_g, alpha,
+                                       ptr(w), dtype_code(wt), w_offset, eps, group, ptr(H_signs), bits, ptr(H_out),
+                                       ld_ho, ptr(X), ld_x, ptr(Xq), ptr(sx), stream_handle()),
+              "hq_norm_rotate_quant")
+    return Xq, sx, H_out, X
+
+
+def hq_lora_max_tiles(M, n):
+    return int(lib.hq_lora_max_tiles(M, n))
+
+
+def hq_lora_plan(ids, n, order=None, tiles=None):
+    """(order int32 [M], tiles int32 [hq_lora_max_tiles(M, n), 3]): the tokens of a
+    batch grouped by their adapter ids int32 [M] in [0, n), -1 for none.  One
+    plan serves every adapted layer of the step."""
+    M = ids.shape[0]
+    _vector(ids, "ids", ids, M, torch.int32)
+    rows = hq_lora_max_tiles(M, n)
+    order = torch.empty((M,), dtype=torch.int32, device=ids.device) if order is None else order
+    tiles = torch.empty((rows, 3), dtype=torch.int32, device=ids.device) if tiles is None else tiles
+    if not ids.is_cuda:
+        raise ValueError("ids must be on a CUDA device")
+    _vector(order, "order", ids, M, torch.int32)
+    _whole(tiles, "tiles", ids, (rows, 3), torch.int32)
+    with torch.cuda.device(ids.device):
+        check(lib.hq_lora_plan(ptr(ids), M, n, ptr(order), ptr(tiles), stream_handle()), "hq_lora_plan")
+    return order, tiles
+
+
+def hq_lora_workspace_size(M, r_max):
+    return int(lib.hq_lora_workspace_size(M, r_max))
+
+
+def hq_lora_apply(X, A, B, order, tiles, ranks=None, scales=None, base=None, Y=None, out_dtype=None, workspace=None):
+    """Y [M, N] = base + scales[a] (X A[a]^T) B[a]^T with a the token's adapter, base
+    alone (zero if None) for a token without one.  A [n, r_max, K] and B
+    [n, N, r_max] have X's type; order and tiles come from hq_lora_plan.  Y may be
+    base (in place); it has base's type, or out_dtype (X's by default)."""
+    M, K = X.shape
+    n, r, N = A.shape[0], A.shape[1], B.shape[1]
+    if Y is None:
+        dt = base.dtype if base is not None else X.dtype if out_dtype is None else out_dtype
+        Y = torch.empty((M, N), dtype=dt, device=X.device)
+    ld_x, ld_y = _rows(X, "X", X, M, K), _rows(Y, "Y", X, M, N, Y.dtype)
+    ld_b = 0 if base is None else _rows(base, "base", X, M, N, Y.dtype)
+    _whole(A, "A", X, (n, r, K), X.dtype)
+    _whole(B, "B", X, (n, N, r), X.dtype)
+    _vector(order, "order", X, M, torch.int32)
+    _whole(tiles, "tiles", X, (hq_lora_max_tiles(M, n), 3), torch.int32)
+    if ranks is not None:
+        _vector(ranks, "ranks", X, n, torch.int32)
+    if scales is not None:
+        _vector(scales, "scales", X, n, torch.float32)
+    with torch.cuda.device(X.device):
+        if workspace is None:
+            workspace = torch.empty((M, r), dtype=torch.float32, device=X.device)
+        elif workspace.device != X.device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the device of X")
+        check(lib.hq_lora_apply(ptr(X), dtype_code(X.dtype), M, K, ld_x, ptr(A), ptr(B), N, n, r, ptr(ranks),
+                                ptr(scales), ptr(order), ptr(tiles), ptr(base), ld_b, ptr(Y), dtype_code(Y.dtype), ld_y,
+                                ptr(workspace), workspace.numel() * workspace.element_size(), stream_handle()),
+              "hq_lora_apply")
+    return Y
+
+
 def hq_last_device_status():
     return int(lib.hq_last_device_status(stream_handle()))
 
@@ -372,6 +529,9 @@ class W4A4Linear:
     pack to int4, pick the r salient input channels from calibration
     activations (largest rotated L2 norm), build SERQ's error matrix.
     ``forward`` is the online path: one rotate/quant launch and one GEMM launch.
+    ``forward_normed`` takes the residual stream instead of the layer's input.
+    ``set_adapters`` puts low-rank adapters beside the layer; a batch's plan
+    (hq_lora_plan) then adds each token's adapter to the output.
     """
 
     def __init__(self, group, gw, H_signs, Wq, sw, zw, Rq, sr, sal_idx, K, N, out_dtype, act_bits=4, offq=False):
@@ -384,6 +544,7 @@ class W4A4Linear:
             raise ValueError("OffQ activations are 4-bit with groups of 128 channels")
         self.act_bits = act_bits
         self.offq = offq
+        self.adapters = None
         self._ws = {}
 
     @staticmethod
@@ -443,17 +604,56 @@ class W4A4Linear:
             self._ws[need] = ws
         return ws
 
-    def forward(self, X, Y=None, Xq=None, sx=None):
+    def set_adapters(self, A, B, ranks=None, scales=None):
+        """Low-rank adapters beside the layer (hq_lora_apply): A [n, r_max, K] on the
+        layer's input, B [n, N, r_max], 16-bit; None takes them away."""
+        if A is None:
+            self.adapters = None
+            return
+        if A.dim() != 3 or A.shape[2] != self.K or B.shape != (A.shape[0], self.N, A.shape[1]):
+            raise ValueError("A must be [n, r_max, %d] and B [n, %d, r_max]" % (self.K, self.N))
+        self.adapters = (A, B, ranks, scales)
+
+    def _adapted(self, X, plan, Y):
+        if plan is None:
+            return Y
+        if self.adapters is None:
+            raise ValueError("the layer has no adapters (set_adapters)")
+        A, B, ranks, scales = self.adapters
+        return hq_lora_apply(X, A, B, plan[0], plan[1], ranks, scales, base=Y, Y=Y)
+
+    def _linear(self, Xq, sx, Y):
+        gemm = w4a8_linear if self.act_bits == 8 else w4a4_linear
+        return gemm(Xq, sx, self.Wq, self.sw, self.zw, self.gw, self.Rq, self.sr, self.sal_idx, self.out_dtype, Y,
+                    self.workspace(Xq.shape[0], Xq.device))
+
+    def forward(self, X, Y=None, Xq=None, sx=None, plan=None):
+        """Y [M, N] of the rows X.  plan = hq_lora_plan(ids, n) adds the adapters of
+        the tokens."""
         if self.offq:
             Xq, sx, zx = hq_rotate_quant_asym(X, self.group, self.H_signs, Xq, sx)
-            return w4a4_linear_asym(Xq, sx, zx, self.Wq, self.sw, self.zw, self.gw, self.Rq, self.sr,
-                                    self.sal_idx, self.out_dtype, Y)
-        if self.act_bits == 8:
-            Xq, sx = hq_rotate_quant8(X, self.group, self.H_signs, Xq, sx)
-            return w4a8_linear(Xq, sx, self.Wq, self.sw, self.zw, self.gw, self.Rq, self.sr, self.sal_idx,
-                               self.out_dtype, Y, self.workspace(X.shape[0], X.device))
-        Xq, sx = hq_rotate_quant(X, self.group, self.H_signs, Xq, sx)
-        return w4a4_linear(Xq, sx, self.Wq, self.sw, self.zw, self.gw, self.Rq, self.sr, self.sal_idx,
-                           self.out_dtype, Y, self.workspace(X.shape[0], X.device))
+            Y = w4a4_linear_asym(Xq, sx, zx, self.Wq, self.sw, self.zw, self.gw, self.Rq, self.sr,
+                                 self.sal_idx, self.out_dtype, Y)
+        else:
+            quant = hq_rotate_quant8 if self.act_bits == 8 else hq_rotate_quant
+            Xq, sx = quant(X, self.group, self.H_signs, Xq, sx)
+            Y = self._linear(Xq, sx, Y)
+        return self._adapted(X, plan, Y)
+
+    def forward_normed(self, H, w, eps, block=None, w_post=None, gate=None, alpha=1.0, w_offset=0.0, Y=None,
+                       H_out=None, plan=None):
+        """(Y, H_out): the layer on the RMS norm (weights w) of the residual stream H
+        updated with the previous block's output, and that stream
+        (hq_residual_norm; H itself without a block).  One launch makes the codes
+        from the stream (hq_norm_rotate_quant); with a norm after the block, or
+        OffQ activations, the normed rows are written and quantised from memory."""
+        if self.offq or w_post is not None:
+            H_out, X = hq_residual_norm(H, w, eps, block, w_post, gate, alpha, w_offset, H_out)
+            Y = self.forward(X, Y, plan=plan)
+        else:
+            Xq, sx, H_out, X = hq_norm_rotate_quant(H, w, eps, self.group, self.H_signs, block, gate, alpha, w_offset,
+                                                    self.act_bits, H_out, want_x=plan is not None)
+            Y = self._adapted(X, plan, self._linear(Xq, sx, Y))
+        return Y, H if H_out is None else H_out
 
     __call__ = forward
