@@ -3,12 +3,14 @@ plain implementations (the plan exactly, the product in 64 bits).
 
 Tolerance of the product, S = sum_k |x_k a_k| and D = sum_j |t_j b_j|:
  * t: an MMA adds 16 exact products to the accumulator with at most 17
-   truncations of 2^-23 of S; a warp does ceil(slabs / 8) of them (64 channels
-   a slab, an eighth of them per block, 16 channels of each per warp), then 4
-   warps and 8 blocks are added: (17 ceil(slabs / 8) + 12) 2^-23 S, and the
-   scale's product 2^-24;
- * t b: t in two tf32 terms is off by 2^-22 of its size, an MMA adds 8 products
-   to the accumulator, 2 MMAs per 8 rank positions: (2^-22 + 18 (r / 8) 2^-23) D;
+   truncations of 2^-23 of S; a warp does at most one per slab of 64 channels (a
+   block has all of K or a part of it), then 4 warps and up to 8 blocks are
+   added: (17 slabs + 12) 2^-23 S, and the scale's product 2^-24;
+ * t b: with 16-bit Y t is two bf16 terms (a nearest bf16 is off by 2^-9, twice:
+   2^-18 of t) and an fp16 b two exact ones, whose product of both second terms
+   (2^-18) is left out: 2^-17 D.  With fp32 Y t is three terms (2^-27) and the
+   product left out 2^-27: 2^-26 D.  At most 5 such MMAs of 17 truncations per
+   16 rank positions: 85 ceil(r / 16) 2^-23 D;
  * the sum with the base row one rounding (2^-24 of its size), the result half a
    step of its type.
 """
@@ -86,7 +88,7 @@ def randn(shape, dt, seed, scale=1.0):
 def batch(M, K, N, n, r, xt, yt, seed=0, ragged=True, runs=1, bare=True):
     rng = np.random.default_rng(seed)
     ids = np.repeat(rng.integers(-1 if bare else 0, n, -(-M // runs)), runs)[:M].astype(np.int32)
-    d = {"ids": torch.from_numpy(ids).cuda(), "X": randn((M, K), xt, seed), "A": randn((n, r, K), xt, seed + 1, K ** -0.5),
+    d = {"yt": yt, "ids": torch.from_numpy(ids).cuda(), "X": randn((M, K), xt, seed), "A": randn((n, r, K), xt, seed + 1, K ** -0.5),
          "B": randn((n, N, r), xt, seed + 2, 0.3), "base": randn((M, N), yt, seed + 3),
          "scales": 0.5 + torch.rand(n, generator=torch.Generator().manual_seed(seed)).cuda(), "ranks": None}
     if ragged:
@@ -110,7 +112,8 @@ def reference(d, base=True):
     y = d["base"].double().clone() if base else torch.zeros(M, N, dtype=torch.float64, device="cuda")
     tol = torch.zeros_like(y)
     slabs = -(-K // 64)
-    steps = 17 * -(-slabs // 8) + 12
+    steps = 17 * slabs + 12
+    split = 2.0 ** -26 if d["yt"] == F32 else 2.0 ** -17
     for a in range(A.shape[0]):
         rows = (ids == a).nonzero().flatten()
         k = A.shape[1] if d["ranks"] is None else int(d["ranks"][a])
@@ -121,7 +124,7 @@ def reference(d, base=True):
         t = s * (X[rows] @ At)
         et = steps * 2.0 ** -23 * s * (X[rows].abs() @ At.abs()) + 2.0 ** -24 * t.abs()
         y[rows] += t @ Bt
-        tol[rows] = et @ Bt.abs() + (2.0 ** -22 + 18 * -(-k // 8) * 2.0 ** -23) * (t.abs() + et) @ Bt.abs()
+        tol[rows] = et @ Bt.abs() + (split + 85 * -(-k // 16) * 2.0 ** -23) * (t.abs() + et) @ Bt.abs()
     return y, tol + 2.0 ** -24 * y.abs()
 
 
@@ -230,7 +233,7 @@ def test_offsets_past_32_bits():
     X.copy_(src)
     order, tiles = hq.hq_lora_plan(ids, n)
     Y = hq.hq_lora_apply(X, A, B, order, tiles, Y=X)      # K = N: the result over the input's rows
-    d = {"X": src, "A": A[-1:], "B": B[-1:], "ids": torch.where(ids < 0, -1, 0), "ranks": None, "scales": None}
+    d = {"X": src, "A": A[-1:], "B": B[-1:], "ids": torch.where(ids < 0, -1, 0), "ranks": None, "scales": None, "yt": F16}
     check(Y, d, base=False)
 
 

@@ -123,12 +123,11 @@ struct ShrinkArgs {
     const uint16_t *X, *A;
     const int32_t *order, *tiles, *ranks;
     const float* scales;
-    float* T;          // [M][r_max] in the plan's order
+    void* T;           // [M][r_max] in the plan's order: fp32, or two bf16 planes
     int64_t ldx;
-    int M, K, n, r;
+    int M, K, n, r, planes;
 };
 
-constexpr int SH_CL = 8;          // CTAs of a cluster, each a run of K
 constexpr int SH_THREADS = 128;
 constexpr int SH_STAGES = 5;
 
@@ -165,6 +164,23 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     return v;
 }
 
+// v as bf16 terms, the first the nearest bf16 and each next one that of the
+// rest (zero where the value is not finite: the first term says it all)
+__device__ __forceinline__ float bf16_near(float v) { return __bfloat162float(__float2bfloat16_rn(v)); }
+__device__ __forceinline__ float rest_of(float v, float near) { return fabsf(near) < INFINITY ? __fsub_rn(v, near) : 0.f; }
+
+__device__ __forceinline__ void put_t(const ShrinkArgs& p, int pos, int col, float v) {
+    const int64_t i = static_cast<int64_t>(pos) * p.r + col;
+    if (p.planes == 0) {
+        static_cast<float*>(p.T)[i] = v;
+    } else {
+        __nv_bfloat16* t = static_cast<__nv_bfloat16*>(p.T);
+        const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+        t[i] = hi;
+        t[i + static_cast<int64_t>(p.M) * p.r] = __float2bfloat16_rn(rest_of(v, __bfloat162float(hi)));
+    }
+}
+
 // One tile and RC columns of the rank per cluster; CTA q of the cluster sums
 // its run of K.  Stages of 64 channels stream through a cp.async ring as
 // 128-byte rows (16-byte chunk c of row i at chunk c ^ (i & 7)); warp w takes
@@ -177,7 +193,7 @@ __global__ void __launch_bounds__(SH_THREADS) k_lora_shrink(const ShrinkArgs p) 
     extern __shared__ __align__(128) uint8_t sm[];
     asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int q = blockIdx.x;   // rank in the cluster
+    const int q = blockIdx.x, cl = gridDim.x;   // rank in the cluster, its CTAs
     const int a = p.tiles[3 * blockIdx.y], start = p.tiles[3 * blockIdx.y + 1], count = p.tiles[3 * blockIdx.y + 2];
     if (a < 0 || count == 0) return;   // no adapter, or an unused tile: the whole cluster leaves
     if (a >= p.n || count < 0 || count > LR_TILE || start < 0 || start > p.M - count) {
@@ -195,8 +211,8 @@ __global__ void __launch_bounds__(SH_THREADS) k_lora_shrink(const ShrinkArgs p) 
     }
     live = min(max(live - r0, 0), RC);
     if (live == 0) {   // the adapter's rank ends before these columns
-        for (int i = q * SH_THREADS + tid; i < count * RC; i += SH_CL * SH_THREADS)
-            if (r0 + i % RC < p.r) p.T[static_cast<int64_t>(start + i / RC) * p.r + r0 + i % RC] = 0.f;
+        for (int i = q * SH_THREADS + tid; i < count * RC; i += cl * SH_THREADS)
+            if (r0 + i % RC < p.r) put_t(p, start + i / RC, r0 + i % RC, 0.f);
         return;
     }
 
@@ -220,8 +236,8 @@ __global__ void __launch_bounds__(SH_THREADS) k_lora_shrink(const ShrinkArgs p) 
     const uint32_t dst = crow * 128 + ((chunk ^ (crow & 7)) << 4);
 
     const int slabs = (p.K + 63) / 64;
-    const int lo = static_cast<int>(static_cast<int64_t>(q) * slabs / SH_CL);
-    const int hi = static_cast<int>(static_cast<int64_t>(q + 1) * slabs / SH_CL);
+    const int lo = static_cast<int>(static_cast<int64_t>(q) * slabs / cl);
+    const int hi = static_cast<int>(static_cast<int64_t>(q + 1) * slabs / cl);
     auto issue = [&](int s, int slot) {
         if (s < hi) {
             const int k = s * 64;
@@ -299,20 +315,18 @@ __global__ void __launch_bounds__(SH_THREADS) k_lora_shrink(const ShrinkArgs p) 
     }
     cluster_sync();
     const float scale = p.scales != nullptr ? p.scales[a] : 1.f;
-    for (int i = q * SH_THREADS + tid; i < count * RC; i += SH_CL * SH_THREADS) {
+    for (int i = q * SH_THREADS + tid; i < count * RC; i += cl * SH_THREADS) {
         float v = 0.f;
-#pragma unroll
-        for (int c = 0; c < SH_CL; ++c) v = __fadd_rn(v, ld_cluster_f32(mapa_shared(smem_u32(part + i), c)));
+        for (int c = 0; c < cl; ++c) v = __fadd_rn(v, ld_cluster_f32(mapa_shared(smem_u32(part + i), c)));
         const int row = i / RC, col = i % RC;
-        if (r0 + col < p.r)
-            p.T[static_cast<int64_t>(start + row) * p.r + r0 + col] = col < live ? __fmul_rn(v, scale) : 0.f;
+        if (r0 + col < p.r) put_t(p, start + row, r0 + col, col < live ? __fmul_rn(v, scale) : 0.f);
     }
     cluster_sync();   // the partial sums stay until every CTA has read them
 }
 
 // ---------------------------------------------------------------------- expand
 struct ExpandArgs {
-    const float* T;
+    const void* T;
     const uint16_t* B;
     const int32_t *order, *tiles, *ranks;
     const void* base;
@@ -321,29 +335,30 @@ struct ExpandArgs {
     int M, N, n, r;
 };
 
-__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
+// Eight consecutive outputs as loaded
+template <int YT>
+struct Out8 {
+    uint4 q[YT == HQ_F32 ? 2 : 1];
+};
 
-__device__ __forceinline__ uint32_t tf32_of(float v) {
-    uint32_t r;
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(v));
-    return r;
+template <int YT>
+__device__ __forceinline__ Out8<YT> ex_load8(const void* p, int64_t i) {
+    Out8<YT> o;
+    constexpr int ES = YT == HQ_F32 ? 4 : 2;
+    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + i * ES);
+#pragma unroll
+    for (int k = 0; k < ES / 2; ++k) o.q[k] = s[k];
+    return o;
 }
 
 template <int YT>
-__device__ __forceinline__ void ex_load8(const void* p, int64_t i, float (&v)[8]) {
+__device__ __forceinline__ void ex_widen(const Out8<YT>& o, float (&v)[8]) {
     if constexpr (YT == HQ_F32) {
-        const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-        const float4 a = s[0], b = s[1];
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        const uint32_t t[8] = {o.q[0].x, o.q[0].y, o.q[0].z, o.q[0].w, o.q[1].x, o.q[1].y, o.q[1].z, o.q[1].w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(t[e]);
     } else {
-        const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-        const uint32_t t[4] = {q.x, q.y, q.z, q.w};
+        const uint32_t t[4] = {o.q[0].x, o.q[0].y, o.q[0].z, o.q[0].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             if constexpr (YT == HQ_BF16) {
@@ -380,128 +395,184 @@ __device__ __forceinline__ void ex_store8(void* p, int64_t i, const float (&v)[8
     }
 }
 
-constexpr int EX_WARPS = 8;
-constexpr int EX_COLS = 32 * EX_WARPS;
+__device__ __forceinline__ uint32_t bf16x2_of(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
 
-// A warp takes 32 output columns of a tile.  The product t B^T runs on the tf32
-// MMA with t split into two tf32 terms (22 bits) and B, a 16-bit value, exact.
+constexpr int EX_WARPS = 4;
+constexpr int EX_COLS = 64 * EX_WARPS;
+
+// A warp takes 64 output columns of a tile.  The product t B^T runs on the
+// bf16 MMA with t as two bf16 terms (16-bit Y: 2^-18 of t, far below Y's own
+// rounding) or three (fp32 Y), and an fp16 B as its two exact bf16 terms; the
+// fp16 MMA would not hold the range of t, and tf32 has a quarter of the rate.
 // Both index orders an MMA leaves open are chosen for the loads: within a chunk
-// of CH rank positions lane t of a quad holds the CH/4 consecutive ones at
-// CH/4 t (one vector load of B and of t), and column c of the i-th n8 tile is
-// column 8 (c / 2) + 2 i + c % 2 of the 32, which leaves each lane 8
+// of R rank positions lane t of a quad holds the R/4 consecutive ones from
+// R/4 t (vector loads of B and of t), and column c of the i-th of four n8
+// tiles is column 8 (c / 2) + 2 i + c % 2 of 32, which leaves each lane 8
 // consecutive outputs of a row, one 16-byte access of base and of Y.
-template <bool BF, int YT, int CH>
+template <bool BF, int YT, int R, bool MULTI>
 __global__ void __launch_bounds__(EX_WARPS * 32) k_lora_expand(const ExpandArgs p) {
-    constexpr int PT = CH / 4;   // rank positions per lane and chunk
+    constexpr int KS = R / 16;               // k16 steps of a chunk
+    constexpr int BT = BF ? 1 : 2;           // terms of B
+    constexpr int TT = YT == HQ_F32 ? 3 : 2; // terms of t
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-    const int n0 = (blockIdx.x * EX_WARPS + warp) * 32;
+    const int n0 = (blockIdx.x * EX_WARPS + warp) * 64;
     const int a = p.tiles[3 * blockIdx.y], start = p.tiles[3 * blockIdx.y + 1], count = p.tiles[3 * blockIdx.y + 2];
-    griddep_wait();
-    if (count <= 0 || count > LR_TILE || start < 0 || start > p.M - count || a >= p.n || n0 >= p.N) return;
-    const int col = n0 + 8 * t4;
-    int live = a < 0 ? 0 : p.r;
-    if (a >= 0 && p.ranks != nullptr) live = min(max(p.ranks[a], 0), p.r);
+    const bool ok = count > 0 && count <= LR_TILE && start >= 0 && start <= p.M - count && a < p.n && n0 < p.N;
+    int live = 0;
+    if (ok && a >= 0) live = p.ranks != nullptr ? min(max(p.ranks[a], 0), p.r) : p.r;
+
+    uint32_t b[BT][2][4][KS][2];   // term, 32 columns, n8 tile, k16 step, register
+    auto load_b = [&](int c) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int nn = n0 + 32 * w + 8 * (g >> 1) + 2 * i + (g & 1);
+                const int j0 = c * R + R / 4 * t4;
+                uint32_t v[KS * 2];
+#pragma unroll
+                for (int e = 0; e < KS * 2; ++e) v[e] = 0u;
+                if (nn < p.N) {
+                    const uint16_t* s = p.B + (static_cast<int64_t>(a) * p.N + nn) * p.r + j0;
+                    if constexpr (R == 16) {
+                        if (j0 < live) {
+                            const uint2 q = __ldg(reinterpret_cast<const uint2*>(s));
+                            v[0] = q.x; v[1] = q.y;
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < KS / 2; ++e)
+                            if (j0 + 8 * e < live) {
+                                const uint4 q = __ldg(reinterpret_cast<const uint4*>(s) + e);
+                                v[4 * e] = q.x; v[4 * e + 1] = q.y; v[4 * e + 2] = q.z; v[4 * e + 3] = q.w;
+                            }
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < KS * 2; ++e) {
+                    // past the adapter's rank B is not read as a number
+                    if (j0 + 2 * e + 1 >= live) v[e] = j0 + 2 * e < live ? v[e] & 0xFFFFu : 0u;
+                    if constexpr (BF) {
+                        b[0][w][i][e / 2][e & 1] = v[e];
+                    } else {
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[e]));
+                        const float h0 = bf16_near(f.x), h1 = bf16_near(f.y);
+                        b[0][w][i][e / 2][e & 1] = bf16x2_of(h0, h1);
+                        b[BT - 1][w][i][e / 2][e & 1] = bf16x2_of(rest_of(f.x, h0), rest_of(f.y, h1));
+                    }
+                }
+            }
+    };
+    if (!MULTI && live > 0) load_b(0);
+    griddep_wait();   // t is complete
+    if (!ok) return;
     if (live == 0 && p.base == p.Y) return;   // in place: the rows stay as they are
+    const int64_t plane = static_cast<int64_t>(p.M) * p.r;
     for (int mt = 0; 16 * mt < count; ++mt) {
         const int i0 = 16 * mt + g;
         int m[2];
+        Out8<YT> y[2][2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             m[h] = i0 + 8 * h < count ? p.order[start + i0 + 8 * h] : -1;
             if (m[h] >= p.M) m[h] = -1;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const int col = n0 + 32 * w + 8 * t4;
+                if (p.base != nullptr && m[h] >= 0 && col < p.N)
+                    y[h][w] = ex_load8<YT>(p.base, m[h] * p.ldb + col);
+                else
+                    y[h][w] = Out8<YT>{};
+            }
         }
-        float y[2][8];
+        float acc[2][4][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int w = 0; w < 2; ++w)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[h][e] = 0.f;
-            if (p.base != nullptr && m[h] >= 0 && col < p.N) ex_load8<YT>(p.base, m[h] * p.ldb + col, y[h]);
-        }
-        float acc[4][4];
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+                for (int e = 0; e < 4; ++e) acc[w][i][e] = 0.f;
+        for (int c = 0; c * R < live; ++c) {
+            if (MULTI) load_b(c);
+            const int j0 = c * R + R / 4 * t4;
+            uint32_t t[TT][KS][4];   // term, step: rows g, g + 8 of the first two positions, then of the last two
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-        for (int c = 0; c * CH < live; ++c) {
-            const int j0 = c * CH + PT * t4;   // this lane's first rank position
-            float tv[2][PT];
+            for (int h = 0; h < 2; ++h) {
+                const int64_t at = static_cast<int64_t>(start + i0 + 8 * h) * p.r + j0;
+                const bool on = i0 + 8 * h < count;
+                if constexpr (YT == HQ_F32) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+                    for (int s = 0; s < KS; ++s) {
+                        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (on && j0 + 4 * s < p.r)
+                            f = *reinterpret_cast<const float4*>(static_cast<const float*>(p.T) + at + 4 * s);
+                        float v[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-                for (int e = 0; e < PT; ++e) tv[h][e] = 0.f;
+                        for (int e = 0; e < TT; ++e) {
+                            const float q[4] = {bf16_near(v[0]), bf16_near(v[1]), bf16_near(v[2]), bf16_near(v[3])};
+                            t[e][s][h] = bf16x2_of(q[0], q[1]);
+                            t[e][s][h + 2] = bf16x2_of(q[2], q[3]);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (i0 + 8 * h < count) {
-                    const float* s = p.T + static_cast<int64_t>(start + i0 + 8 * h) * p.r + j0;
-                    if constexpr (PT == 2) {
-                        const float2 v = *reinterpret_cast<const float2*>(s);
-                        tv[h][0] = v.x; tv[h][1] = v.y;
-                    } else {
+                            for (int k = 0; k < 4; ++k) v[k] = rest_of(v[k], q[k]);
+                        }
+                    }
+                } else {
 #pragma unroll
-                        for (int e = 0; e < PT; e += 4) {
-                            const float4 v = *reinterpret_cast<const float4*>(s + e);
-                            tv[h][e] = v.x; tv[h][e + 1] = v.y; tv[h][e + 2] = v.z; tv[h][e + 3] = v.w;
+                    for (int e = 0; e < TT; ++e) {
+                        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.T) + e * plane + at;
+                        if constexpr (R == 16) {
+                            uint2 q = make_uint2(0u, 0u);
+                            if (on && j0 < p.r) q = *reinterpret_cast<const uint2*>(src);
+                            t[e][0][h] = q.x;
+                            t[e][0][h + 2] = q.y;
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < KS / 2; ++k) {
+                                uint4 q = make_uint4(0u, 0u, 0u, 0u);
+                                if (on && j0 + 8 * k < p.r) q = *reinterpret_cast<const uint4*>(src + 8 * k);
+                                t[e][2 * k][h] = q.x;
+                                t[e][2 * k][h + 2] = q.y;
+                                t[e][2 * k + 1][h] = q.z;
+                                t[e][2 * k + 1][h + 2] = q.w;
+                            }
                         }
                     }
                 }
-            uint32_t bw[4][PT / 2];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int nn = n0 + 8 * (g >> 1) + 2 * i + (g & 1);
-#pragma unroll
-                for (int e = 0; e < PT / 2; ++e) bw[i][e] = 0u;
-                if (nn < p.N) {
-                    const uint16_t* s = p.B + (static_cast<int64_t>(a) * p.N + nn) * p.r + j0;
-                    if constexpr (PT == 2) {
-                        bw[i][0] = __ldg(reinterpret_cast<const uint32_t*>(s));
-                    } else if constexpr (PT == 4) {
-                        const uint2 v = __ldg(reinterpret_cast<const uint2*>(s));
-                        bw[i][0] = v.x; bw[i][1] = v.y;
-                    } else {
-                        const uint4 v = __ldg(reinterpret_cast<const uint4*>(s));
-                        bw[i][0] = v.x; bw[i][1] = v.y; bw[i][2] = v.z; bw[i][3] = v.w;
-                    }
-                }
             }
+            // small terms first; the product of both last terms is below fp32
 #pragma unroll
-            for (int s = 0; s < PT / 2; ++s) {   // k = t: position 2 s, k = t + 4: position 2 s + 1
-                uint32_t hi[4], lo[4];
+            for (int e = TT - 1; e >= 0; --e)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float v = tv[e & 1][2 * s + (e >> 1)];
-                    hi[e] = tf32_of(v);
-                    lo[e] = fabsf(v) < INFINITY ? tf32_of(__fsub_rn(v, __uint_as_float(hi[e]))) : 0u;
-                }
-                // past the adapter's rank t is zero; B there is not read as a number
-                const bool ok0 = j0 + 2 * s < live, ok1 = j0 + 2 * s + 1 < live;
+                for (int f = BT - 1; f >= 0; --f)
+                    if (e + f < TT)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t w = bw[i][s];
-                    float b0, b1;
-                    if constexpr (BF) {
-                        b0 = __uint_as_float(w << 16);
-                        b1 = __uint_as_float(w & 0xFFFF0000u);
-                    } else {
-                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-                        b0 = f.x;
-                        b1 = f.y;
-                    }
-                    const uint32_t u0 = ok0 ? __float_as_uint(b0) : 0u, u1 = ok1 ? __float_as_uint(b1) : 0u;
-                    mma_tf32(acc[i], lo, u0, u1);
-                    mma_tf32(acc[i], hi, u0, u1);
-                }
-            }
+                        for (int s = 0; s < KS; ++s)
+#pragma unroll
+                            for (int w = 0; w < 2; ++w)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    mma_16x8x16<true>(acc[w][i], t[e][s], b[f][w][i][s][0], b[f][w][i][s][1]);
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            if (m[h] >= 0 && col < p.N) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+            for (int w = 0; w < 2; ++w) {
+                const int col = n0 + 32 * w + 8 * t4;
+                if (m[h] >= 0 && col < p.N) {
+                    float v[8];
+                    ex_widen<YT>(y[h][w], v);
                     if (live > 0) {
-                        y[h][2 * i] = __fadd_rn(y[h][2 * i], acc[i][2 * h]);
-                        y[h][2 * i + 1] = __fadd_rn(y[h][2 * i + 1], acc[i][2 * h + 1]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            v[2 * i] = __fadd_rn(v[2 * i], acc[w][i][2 * h]);
+                            v[2 * i + 1] = __fadd_rn(v[2 * i + 1], acc[w][i][2 * h + 1]);
+                        }
                     }
-                ex_store8<YT>(p.Y, m[h] * p.ldy + col, y[h]);
+                    ex_store8<YT>(p.Y, m[h] * p.ldy + col, v);
+                }
             }
     }
 }
@@ -514,14 +585,17 @@ hq_status launch_shrink(const ShrinkArgs& a, int tiles, cudaStream_t st) {
     constexpr int smem = ring > part ? ring : part;
     auto kern = k_lora_shrink<BF, RC>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return HQ_ERR_CUDA;
+    // K is cut as far as one wave of CTAs (two per SM) goes
+    const int z = (a.r + RC - 1) / RC;
+    const int cl = tiles * z <= 37 ? 8 : tiles * z <= 74 ? 4 : tiles * z <= 148 ? 2 : 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(SH_CL, tiles, (a.r + RC - 1) / RC);
+    cfg.gridDim = dim3(cl, tiles, z);
     cfg.blockDim = dim3(SH_THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = SH_CL;
+    attr[0].val.clusterDim.x = cl;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
@@ -542,12 +616,14 @@ hq_status launch_expand(const ExpandArgs& a, int tiles, cudaStream_t st) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cudaError_t e;
-    if (a.r % 32 == 0)
-        e = cudaLaunchKernelEx(&cfg, k_lora_expand<BF, YT, 32>, a);
-    else if (a.r % 16 == 0)
-        e = cudaLaunchKernelEx(&cfg, k_lora_expand<BF, YT, 16>, a);
+    if (a.r <= 16)
+        e = cudaLaunchKernelEx(&cfg, k_lora_expand<BF, YT, 16, false>, a);
+    else if (a.r <= 32)
+        e = cudaLaunchKernelEx(&cfg, k_lora_expand<BF, YT, 32, false>, a);
+    else if (BF && YT != HQ_F32 && a.r <= 64)   // B's fragments for the whole rank fit the registers
+        e = cudaLaunchKernelEx(&cfg, k_lora_expand<BF, YT, BF && YT != HQ_F32 ? 64 : 32, false>, a);
     else
-        e = cudaLaunchKernelEx(&cfg, k_lora_expand<BF, YT, 8>, a);
+        e = cudaLaunchKernelEx(&cfg, k_lora_expand<BF, YT, 32, true>, a);
     return e == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
 }
 
@@ -622,7 +698,8 @@ extern "C" hq_status hq_lora_apply(const void* X, hq_dtype xt, int64_t M, int64_
     s.X = static_cast<const uint16_t*>(X);
     s.A = static_cast<const uint16_t*>(A);
     s.order = order; s.tiles = tiles; s.ranks = ranks; s.scales = scales;
-    s.T = static_cast<float*>(workspace);
+    s.T = workspace;
+    s.planes = yt == HQ_F32 ? 0 : 2;
     s.ldx = ld_x;
     s.M = static_cast<int>(M); s.K = static_cast<int>(K); s.n = static_cast<int>(n); s.r = r_max;
     ExpandArgs e = {};
