@@ -130,6 +130,12 @@ struct ShrinkArgs {
 
 constexpr int SH_THREADS = 128;
 constexpr int SH_STAGES = 5;
+constexpr int SH_MAX_CL = 8;      // CTAs of a cluster, each a run of K
+
+// 8-byte asynchronous global -> shared copy
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
+}
 
 // 16-byte asynchronous copy; bytes past `bytes` (0 or 16) are written as zero
 __device__ __forceinline__ void cp_async16_z(uint32_t dst, const void* src, int bytes) {
@@ -158,10 +164,22 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], const uint32_t (&a)[4
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
+}
+
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+    return make_float4(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y), __fadd_rn(a.z, b.z), __fadd_rn(a.w, b.w));
+}
+
+__device__ __forceinline__ uint32_t bf16x2_of(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // v as bf16 terms, the first the nearest bf16 and each next one that of the
@@ -169,15 +187,17 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
 __device__ __forceinline__ float bf16_near(float v) { return __bfloat162float(__float2bfloat16_rn(v)); }
 __device__ __forceinline__ float rest_of(float v, float near) { return fabsf(near) < INFINITY ? __fsub_rn(v, near) : 0.f; }
 
-__device__ __forceinline__ void put_t(const ShrinkArgs& p, int pos, int col, float v) {
+// Stores t of four rank positions of one token: fp32, or as two bf16 planes
+__device__ __forceinline__ void put_t(const ShrinkArgs& p, int pos, int col, float4 v) {
     const int64_t i = static_cast<int64_t>(pos) * p.r + col;
     if (p.planes == 0) {
-        static_cast<float*>(p.T)[i] = v;
+        *reinterpret_cast<float4*>(static_cast<float*>(p.T) + i) = v;
     } else {
-        __nv_bfloat16* t = static_cast<__nv_bfloat16*>(p.T);
-        const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-        t[i] = hi;
-        t[i + static_cast<int64_t>(p.M) * p.r] = __float2bfloat16_rn(rest_of(v, __bfloat162float(hi)));
+        uint16_t* t = static_cast<uint16_t*>(p.T);
+        const float4 n = make_float4(bf16_near(v.x), bf16_near(v.y), bf16_near(v.z), bf16_near(v.w));
+        *reinterpret_cast<uint2*>(t + i) = make_uint2(bf16x2_of(n.x, n.y), bf16x2_of(n.z, n.w));
+        *reinterpret_cast<uint2*>(t + i + static_cast<int64_t>(p.M) * p.r) =
+            make_uint2(bf16x2_of(rest_of(v.x, n.x), rest_of(v.y, n.y)), bf16x2_of(rest_of(v.z, n.z), rest_of(v.w, n.w)));
     }
 }
 
@@ -211,8 +231,10 @@ __global__ void __launch_bounds__(SH_THREADS) k_lora_shrink(const ShrinkArgs p) 
     }
     live = min(max(live - r0, 0), RC);
     if (live == 0) {   // the adapter's rank ends before these columns
-        for (int i = q * SH_THREADS + tid; i < count * RC; i += cl * SH_THREADS)
-            if (r0 + i % RC < p.r) put_t(p, start + i / RC, r0 + i % RC, 0.f);
+        for (int i = q * SH_THREADS + tid; i < count * (RC / 4); i += cl * SH_THREADS) {
+            const int row = i / (RC / 4), col = r0 + i % (RC / 4) * 4;
+            if (col < p.r) put_t(p, start + row, col, make_float4(0.f, 0.f, 0.f, 0.f));
+        }
         return;
     }
 
@@ -307,19 +329,30 @@ __global__ void __launch_bounds__(SH_THREADS) k_lora_shrink(const ShrinkArgs p) 
             *reinterpret_cast<float2*>(d + 8 * RC) = make_float2(acc[mt][i][2], acc[mt][i][3]);
         }
     __syncthreads();
-    for (int i = tid; i < count * RC; i += SH_THREADS) {
-        float v = part[i];
+    float4* part4 = reinterpret_cast<float4*>(sm);
+    for (int i = tid; i < count * (RC / 4); i += SH_THREADS) {
+        float4 v = part4[i];
 #pragma unroll
-        for (int w = 1; w < SH_THREADS / 32; ++w) v = __fadd_rn(v, part[w * LR_TILE * RC + i]);
-        part[i] = v;
+        for (int w = 1; w < SH_THREADS / 32; ++w) v = add4(v, part4[w * LR_TILE * (RC / 4) + i]);
+        part4[i] = v;
     }
     cluster_sync();
     const float scale = p.scales != nullptr ? p.scales[a] : 1.f;
-    for (int i = q * SH_THREADS + tid; i < count * RC; i += cl * SH_THREADS) {
-        float v = 0.f;
-        for (int c = 0; c < cl; ++c) v = __fadd_rn(v, ld_cluster_f32(mapa_shared(smem_u32(part + i), c)));
-        const int row = i / RC, col = i % RC;
-        if (r0 + col < p.r) put_t(p, start + row, r0 + col, col < live ? __fmul_rn(v, scale) : 0.f);
+    for (int i = q * SH_THREADS + tid; i < count * (RC / 4); i += cl * SH_THREADS) {
+        float4 u[SH_MAX_CL];   // all on their way before the first sum
+#pragma unroll
+        for (int c = 0; c < SH_MAX_CL; ++c)
+            if (c < cl) u[c] = ld_cluster_f32x4(mapa_shared(smem_u32(part4 + i), c));
+        float4 v = u[0];
+#pragma unroll
+        for (int c = 1; c < SH_MAX_CL; ++c)
+            if (c < cl) v = add4(v, u[c]);
+        const int row = i / (RC / 4), col = i % (RC / 4) * 4;
+        v.x = col < live ? __fmul_rn(v.x, scale) : 0.f;
+        v.y = col + 1 < live ? __fmul_rn(v.y, scale) : 0.f;
+        v.z = col + 2 < live ? __fmul_rn(v.z, scale) : 0.f;
+        v.w = col + 3 < live ? __fmul_rn(v.w, scale) : 0.f;
+        if (r0 + col < p.r) put_t(p, start + row, r0 + col, v);
     }
     cluster_sync();   // the partial sums stay until every CTA has read them
 }
@@ -340,16 +373,6 @@ template <int YT>
 struct Out8 {
     uint4 q[YT == HQ_F32 ? 2 : 1];
 };
-
-template <int YT>
-__device__ __forceinline__ Out8<YT> ex_load8(const void* p, int64_t i) {
-    Out8<YT> o;
-    constexpr int ES = YT == HQ_F32 ? 4 : 2;
-    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + i * ES);
-#pragma unroll
-    for (int k = 0; k < ES / 2; ++k) o.q[k] = s[k];
-    return o;
-}
 
 template <int YT>
 __device__ __forceinline__ void ex_widen(const Out8<YT>& o, float (&v)[8]) {
@@ -395,11 +418,6 @@ __device__ __forceinline__ void ex_store8(void* p, int64_t i, const float (&v)[8
     }
 }
 
-__device__ __forceinline__ uint32_t bf16x2_of(float a, float b) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 constexpr int EX_WARPS = 4;
 constexpr int EX_COLS = 64 * EX_WARPS;
 
@@ -417,10 +435,11 @@ __global__ void __launch_bounds__(EX_WARPS * 32) k_lora_expand(const ExpandArgs 
     constexpr int KS = R / 16;               // k16 steps of a chunk
     constexpr int BT = BF ? 1 : 2;           // terms of B
     constexpr int TT = YT == HQ_F32 ? 3 : 2; // terms of t
+    extern __shared__ __align__(128) uint8_t sm[];   // t: [term][64][trow], then the base slots
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const int n0 = (blockIdx.x * EX_WARPS + warp) * 64;
     const int a = p.tiles[3 * blockIdx.y], start = p.tiles[3 * blockIdx.y + 1], count = p.tiles[3 * blockIdx.y + 2];
-    const bool ok = count > 0 && count <= LR_TILE && start >= 0 && start <= p.M - count && a < p.n && n0 < p.N;
+    const bool ok = count > 0 && count <= LR_TILE && start >= 0 && start <= p.M - count && a < p.n;
     int live = 0;
     if (ok && a >= 0) live = p.ranks != nullptr ? min(max(p.ranks[a], 0), p.r) : p.r;
 
@@ -466,28 +485,73 @@ __global__ void __launch_bounds__(EX_WARPS * 32) k_lora_expand(const ExpandArgs 
                 }
             }
     };
-    if (!MULTI && live > 0) load_b(0);
-    griddep_wait();   // t is complete
-    if (!ok) return;
-    if (live == 0 && p.base == p.Y) return;   // in place: the rows stay as they are
-    const int64_t plane = static_cast<int64_t>(p.M) * p.r;
-    for (int mt = 0; 16 * mt < count; ++mt) {
-        const int i0 = 16 * mt + g;
-        int m[2];
-        Out8<YT> y[2][2];
+    // this lane's base rows, on their way to slots of its own before t is awaited
+    const int rp = (p.r + R - 1) / R * R, trow = 2 * rp + 8;   // bytes of a staged row of t
+    uint8_t* slots = sm + TT * LR_TILE * trow + (warp * 32 + lane) * 16;
+    constexpr int PIECES = YT == HQ_F32 ? 2 : 1;
+    constexpr int SLOT = EX_WARPS * 32 * 16;   // from one piece of a lane to its next
+    int m[LR_TILE / 16][2];
+#pragma unroll
+    for (int mt = 0; mt < LR_TILE / 16; ++mt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            m[h] = i0 + 8 * h < count ? p.order[start + i0 + 8 * h] : -1;
-            if (m[h] >= p.M) m[h] = -1;
+            const int i = 16 * mt + 8 * h + g;
+            m[mt][h] = ok && i < count ? p.order[start + i] : -1;
+            if (m[mt][h] >= p.M) m[mt][h] = -1;
+        }
+    const bool keep = !ok || (live == 0 && p.base == p.Y);   // nothing to do: in place the rows stay as they are
+    if (p.base != nullptr && !keep) {
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                const int col = n0 + 32 * w + 8 * t4;
-                if (p.base != nullptr && m[h] >= 0 && col < p.N)
-                    y[h][w] = ex_load8<YT>(p.base, m[h] * p.ldb + col);
-                else
-                    y[h][w] = Out8<YT>{};
+        for (int mt = 0; mt < LR_TILE / 16; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const int col = n0 + 32 * w + 8 * t4;
+                    if (m[mt][h] >= 0 && col < p.N) {
+                        const uint8_t* src = static_cast<const uint8_t*>(p.base) + (m[mt][h] * p.ldb + col) * (PIECES * 2);
+#pragma unroll
+                        for (int e = 0; e < PIECES; ++e)
+                            cp_async16(smem_u32(slots + (((mt * 2 + h) * 2 + w) * PIECES + e) * SLOT), src + 16 * e);
+                    }
+                }
+    }
+    if (!MULTI && live > 0) load_b(0);
+    griddep_wait();   // t is complete
+    if (live > 0) {   // the same for the whole CTA
+        const int64_t plane = static_cast<int64_t>(p.M) * p.r;
+        const int per = rp / 4;   // groups of four rank positions
+        for (int i = threadIdx.x; i < count * per; i += EX_WARPS * 32) {
+            const int row = i / per, j = i % per * 4;
+            const int64_t at = static_cast<int64_t>(start + row) * p.r + j;
+            uint8_t* dst = sm + row * trow + 2 * j;
+            if (j >= p.r) {
+#pragma unroll
+                for (int e = 0; e < TT; ++e) *reinterpret_cast<uint2*>(dst + e * LR_TILE * trow) = make_uint2(0u, 0u);
+            } else if constexpr (YT == HQ_F32) {
+                const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(p.T) + at);
+                float v[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                for (int e = 0; e < TT; ++e) {
+                    const float q[4] = {bf16_near(v[0]), bf16_near(v[1]), bf16_near(v[2]), bf16_near(v[3])};
+                    *reinterpret_cast<uint2*>(dst + e * LR_TILE * trow) =
+                        make_uint2(bf16x2_of(q[0], q[1]), bf16x2_of(q[2], q[3]));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] = rest_of(v[k], q[k]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < TT; ++e)
+                    cp_async8(smem_u32(dst + e * LR_TILE * trow), static_cast<const uint16_t*>(p.T) + e * plane + at);
             }
         }
+    }
+    cp_async_wait_all();
+    __syncthreads();
+    if (keep) return;
+#pragma unroll
+    for (int mt = 0; mt < LR_TILE / 16; ++mt) {
+        if (16 * mt >= count) break;
         float acc[2][4][4];
 #pragma unroll
         for (int w = 0; w < 2; ++w)
@@ -497,73 +561,39 @@ __global__ void __launch_bounds__(EX_WARPS * 32) k_lora_expand(const ExpandArgs 
                 for (int e = 0; e < 4; ++e) acc[w][i][e] = 0.f;
         for (int c = 0; c * R < live; ++c) {
             if (MULTI) load_b(c);
-            const int j0 = c * R + R / 4 * t4;
-            uint32_t t[TT][KS][4];   // term, step: rows g, g + 8 of the first two positions, then of the last two
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t at = static_cast<int64_t>(start + i0 + 8 * h) * p.r + j0;
-                const bool on = i0 + 8 * h < count;
-                if constexpr (YT == HQ_F32) {
-#pragma unroll
-                    for (int s = 0; s < KS; ++s) {
-                        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (on && j0 + 4 * s < p.r)
-                            f = *reinterpret_cast<const float4*>(static_cast<const float*>(p.T) + at + 4 * s);
-                        float v[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-                        for (int e = 0; e < TT; ++e) {
-                            const float q[4] = {bf16_near(v[0]), bf16_near(v[1]), bf16_near(v[2]), bf16_near(v[3])};
-                            t[e][s][h] = bf16x2_of(q[0], q[1]);
-                            t[e][s][h + 2] = bf16x2_of(q[2], q[3]);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) v[k] = rest_of(v[k], q[k]);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < TT; ++e) {
-                        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.T) + e * plane + at;
-                        if constexpr (R == 16) {
-                            uint2 q = make_uint2(0u, 0u);
-                            if (on && j0 < p.r) q = *reinterpret_cast<const uint2*>(src);
-                            t[e][0][h] = q.x;
-                            t[e][0][h + 2] = q.y;
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < KS / 2; ++k) {
-                                uint4 q = make_uint4(0u, 0u, 0u, 0u);
-                                if (on && j0 + 8 * k < p.r) q = *reinterpret_cast<const uint4*>(src + 8 * k);
-                                t[e][2 * k][h] = q.x;
-                                t[e][2 * k][h + 2] = q.y;
-                                t[e][2 * k + 1][h] = q.z;
-                                t[e][2 * k + 1][h + 2] = q.w;
-                            }
-                        }
-                    }
-                }
-            }
-            // small terms first; the product of both last terms is below fp32
+            // small terms first; the product of both last terms is left out
 #pragma unroll
             for (int e = TT - 1; e >= 0; --e)
 #pragma unroll
-                for (int f = BT - 1; f >= 0; --f)
-                    if (e + f < TT)
+                for (int s = 0; s < KS; ++s) {
+                    const uint8_t* src = sm + (e * LR_TILE + 16 * mt + g) * trow + 2 * (c * R + R / 4 * t4 + 4 * s);
+                    const uint2 q0 = *reinterpret_cast<const uint2*>(src);
+                    const uint2 q1 = *reinterpret_cast<const uint2*>(src + 8 * trow);
+                    const uint32_t t[4] = {q0.x, q1.x, q0.y, q1.y};
 #pragma unroll
-                        for (int s = 0; s < KS; ++s)
+                    for (int f = BT - 1; f >= 0; --f)
+                        if (e + f < TT)
 #pragma unroll
                             for (int w = 0; w < 2; ++w)
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
-                                    mma_16x8x16<true>(acc[w][i], t[e][s], b[f][w][i][s][0], b[f][w][i][s][1]);
+                                    mma_16x8x16<true>(acc[w][i], t, b[f][w][i][s][0], b[f][w][i][s][1]);
+                }
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
                 const int col = n0 + 32 * w + 8 * t4;
-                if (m[h] >= 0 && col < p.N) {
-                    float v[8];
-                    ex_widen<YT>(y[h][w], v);
+                if (m[mt][h] >= 0 && col < p.N) {
+                    float v[8] = {};
+                    if (p.base != nullptr) {
+                        Out8<YT> y;
+#pragma unroll
+                        for (int e = 0; e < PIECES; ++e)
+                            y.q[e] = *reinterpret_cast<const uint4*>(slots + (((mt * 2 + h) * 2 + w) * PIECES + e) * SLOT);
+                        ex_widen<YT>(y, v);
+                    }
                     if (live > 0) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -571,7 +601,7 @@ __global__ void __launch_bounds__(EX_WARPS * 32) k_lora_expand(const ExpandArgs 
                             v[2 * i + 1] = __fadd_rn(v[2 * i + 1], acc[w][i][2 * h + 1]);
                         }
                     }
-                    ex_store8<YT>(p.Y, m[h] * p.ldy + col, v);
+                    ex_store8<YT>(p.Y, m[mt][h] * p.ldy + col, v);
                 }
             }
     }
@@ -603,11 +633,16 @@ hq_status launch_shrink(const ShrinkArgs& a, int tiles, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
 }
 
-template <bool BF, int YT>
-hq_status launch_expand(const ExpandArgs& a, int tiles, cudaStream_t st) {
+template <bool BF, int YT, int R, bool MULTI>
+hq_status launch_expand_r(const ExpandArgs& a, int tiles, cudaStream_t st) {
+    const int rp = (a.r + R - 1) / R * R;
+    const int smem = (YT == HQ_F32 ? 3 : 2) * LR_TILE * (2 * rp + 8) + EX_WARPS * 32 * 16 * 16 * (YT == HQ_F32 ? 2 : 1);
+    auto kern = k_lora_expand<BF, YT, R, MULTI>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return HQ_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((a.N + EX_COLS - 1) / EX_COLS, tiles);
     cfg.blockDim = dim3(EX_WARPS * 32);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     // may start while k_lora_shrink runs; it waits for that grid's completion
     cudaLaunchAttribute attr[1];
@@ -615,16 +650,19 @@ hq_status launch_expand(const ExpandArgs& a, int tiles, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e;
-    if (a.r <= 16)
-        e = cudaLaunchKernelEx(&cfg, k_lora_expand<BF, YT, 16, false>, a);
-    else if (a.r <= 32)
-        e = cudaLaunchKernelEx(&cfg, k_lora_expand<BF, YT, 32, false>, a);
-    else if (BF && YT != HQ_F32 && a.r <= 64)   // B's fragments for the whole rank fit the registers
-        e = cudaLaunchKernelEx(&cfg, k_lora_expand<BF, YT, BF && YT != HQ_F32 ? 64 : 32, false>, a);
-    else
-        e = cudaLaunchKernelEx(&cfg, k_lora_expand<BF, YT, 32, true>, a);
-    return e == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
+}
+
+// B's fragments stay in registers for a whole tile where the rank fits: 64
+// positions of a 16-bit B used as it is, 32 where B has two terms or t three
+template <bool BF, int YT>
+hq_status launch_expand(const ExpandArgs& a, int tiles, cudaStream_t st) {
+    if (a.r <= 16) return launch_expand_r<BF, YT, 16, false>(a, tiles, st);
+    if (a.r <= 32) return launch_expand_r<BF, YT, 32, false>(a, tiles, st);
+    if constexpr (BF && YT != HQ_F32) {
+        if (a.r <= 64) return launch_expand_r<BF, YT, 64, false>(a, tiles, st);
+    }
+    return launch_expand_r<BF, YT, 32, true>(a, tiles, st);
 }
 
 template <bool BF>
