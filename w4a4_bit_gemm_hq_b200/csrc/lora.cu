@@ -123,19 +123,14 @@ struct ShrinkArgs {
     const uint16_t *X, *A;
     const int32_t *order, *tiles, *ranks;
     const float* scales;
-    void* T;           // [M][r_max] in the plan's order: fp32, or two bf16 planes
+    float* T;          // [M][r_max] in the plan's order
     int64_t ldx;
-    int M, K, n, r, planes;
+    int M, K, n, r;
 };
 
-constexpr int SH_THREADS = 128;
-constexpr int SH_STAGES = 5;
+constexpr int SH_THREADS = 256;
+constexpr int SH_STAGES = 3;
 constexpr int SH_MAX_CL = 8;      // CTAs of a cluster, each a run of K
-
-// 8-byte asynchronous global -> shared copy
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
-}
 
 // 16-byte asynchronous copy; bytes past `bytes` (0 or 16) are written as zero
 __device__ __forceinline__ void cp_async16_z(uint32_t dst, const void* src, int bytes) {
@@ -177,39 +172,15 @@ __device__ __forceinline__ float4 add4(float4 a, float4 b) {
     return make_float4(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y), __fadd_rn(a.z, b.z), __fadd_rn(a.w, b.w));
 }
 
-__device__ __forceinline__ uint32_t bf16x2_of(float a, float b) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// v as bf16 terms, the first the nearest bf16 and each next one that of the
-// rest (zero where the value is not finite: the first term says it all)
-__device__ __forceinline__ float bf16_near(float v) { return __bfloat162float(__float2bfloat16_rn(v)); }
-__device__ __forceinline__ float rest_of(float v, float near) { return fabsf(near) < INFINITY ? __fsub_rn(v, near) : 0.f; }
-
-// Stores t of four rank positions of one token: fp32, or as two bf16 planes
-__device__ __forceinline__ void put_t(const ShrinkArgs& p, int pos, int col, float4 v) {
-    const int64_t i = static_cast<int64_t>(pos) * p.r + col;
-    if (p.planes == 0) {
-        *reinterpret_cast<float4*>(static_cast<float*>(p.T) + i) = v;
-    } else {
-        uint16_t* t = static_cast<uint16_t*>(p.T);
-        const float4 n = make_float4(bf16_near(v.x), bf16_near(v.y), bf16_near(v.z), bf16_near(v.w));
-        *reinterpret_cast<uint2*>(t + i) = make_uint2(bf16x2_of(n.x, n.y), bf16x2_of(n.z, n.w));
-        *reinterpret_cast<uint2*>(t + i + static_cast<int64_t>(p.M) * p.r) =
-            make_uint2(bf16x2_of(rest_of(v.x, n.x), rest_of(v.y, n.y)), bf16x2_of(rest_of(v.z, n.z), rest_of(v.w, n.w)));
-    }
-}
-
 // One tile and RC columns of the rank per cluster; CTA q of the cluster sums
-// its run of K.  Stages of 64 channels stream through a cp.async ring as
-// 128-byte rows (16-byte chunk c of row i at chunk c ^ (i & 7)); warp w takes
-// channels 16 w .. 16 w + 15 of every stage for all of the tile's tokens, so
-// each staged byte is read from shared memory once.  The partial sums meet in
-// a fixed order: over the CTA's warps, then over the cluster.
+// its run of K.  Stages of 128 channels stream through a cp.async ring as two
+// halves of 128-byte rows (16-byte chunk c of row i at chunk c ^ (i & 7)).
+// Warp (h, w) takes 32 of the tile's tokens and channels 16 w .. 16 w + 15 of
+// each half.  The partial sums meet in a fixed order: over the CTA's warps,
+// then over the cluster.
 template <bool BF, int RC>
 __global__ void __launch_bounds__(SH_THREADS) k_lora_shrink(const ShrinkArgs p) {
-    constexpr int STAGE = (LR_TILE + RC) * 128;
+    constexpr int HALF = (LR_TILE + RC) * 128, STAGE = 2 * HALF;
     extern __shared__ __align__(128) uint8_t sm[];
     asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -233,13 +204,14 @@ __global__ void __launch_bounds__(SH_THREADS) k_lora_shrink(const ShrinkArgs p) 
     if (live == 0) {   // the adapter's rank ends before these columns
         for (int i = q * SH_THREADS + tid; i < count * (RC / 4); i += cl * SH_THREADS) {
             const int row = i / (RC / 4), col = r0 + i % (RC / 4) * 4;
-            if (col < p.r) put_t(p, start + row, col, make_float4(0.f, 0.f, 0.f, 0.f));
+            if (col < p.r)
+                *reinterpret_cast<float4*>(p.T + static_cast<int64_t>(start + row) * p.r + col) = make_float4(0.f, 0.f, 0.f, 0.f);
         }
         return;
     }
 
-    // this thread's rows of a stage: tokens tid/8 + 16 j, adapter rows the same
-    const int crow = tid >> 3, chunk = tid & 7;
+    // this thread's rows of a stage: tokens tid/16 + 16 j, adapter rows the same
+    const int crow = tid >> 4, chunk = tid & 15;
     const uint16_t* xsrc[LR_TILE / 16];
 #pragma unroll
     for (int j = 0; j < LR_TILE / 16; ++j) {
@@ -255,14 +227,14 @@ __global__ void __launch_bounds__(SH_THREADS) k_lora_shrink(const ShrinkArgs p) 
     }
     const uint16_t* asrc = p.A + (static_cast<int64_t>(a) * p.r + r0 + crow) * p.K + chunk * 8;
     const uint32_t ring = smem_u32(sm);
-    const uint32_t dst = crow * 128 + ((chunk ^ (crow & 7)) << 4);
+    const uint32_t dst = (chunk >> 3) * HALF + crow * 128 + (((chunk & 7) ^ (crow & 7)) << 4);
 
-    const int slabs = (p.K + 63) / 64;
+    const int slabs = (p.K + 127) / 128;
     const int lo = static_cast<int>(static_cast<int64_t>(q) * slabs / cl);
     const int hi = static_cast<int>(static_cast<int64_t>(q + 1) * slabs / cl);
     auto issue = [&](int s, int slot) {
         if (s < hi) {
-            const int k = s * 64;
+            const int k = s * 128;
             const int bytes = k + chunk * 8 < p.K ? 16 : 0;   // K is a multiple of 8
             const uint32_t base = ring + slot * STAGE + dst;
 #pragma unroll
@@ -278,18 +250,19 @@ __global__ void __launch_bounds__(SH_THREADS) k_lora_shrink(const ShrinkArgs p) 
         cp_async_commit();
     };
 
-    float acc[LR_TILE / 16][RC / 8][4];
+    float acc[2][RC / 8][4];
 #pragma unroll
-    for (int mt = 0; mt < LR_TILE / 16; ++mt)
+    for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
         for (int i = 0; i < RC / 8; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[mt][i][e] = 0.f;
 
-    // ldmatrix addresses within a stage: tokens (16 x 16) and adapter rows (two n8 x k16)
-    const int am = lane & 15, ac = 2 * warp + (lane >> 4);
-    const int bn = (lane & 7) + ((lane >> 4) << 3), bc = 2 * warp + ((lane >> 3) & 1);
-    const uint32_t aoff = am * 128 + ((ac ^ (am & 7)) << 4);
+    // ldmatrix addresses within half a stage: tokens (16 x 16) and adapter rows (two n8 x k16)
+    const int wk = warp & 3, m0 = (warp >> 2) * 32;
+    const int am = lane & 15, ac = 2 * wk + (lane >> 4);
+    const int bn = (lane & 7) + ((lane >> 4) << 3), bc = 2 * wk + ((lane >> 3) & 1);
+    const uint32_t aoff = (m0 + am) * 128 + ((ac ^ (am & 7)) << 4);
     const uint32_t boff = LR_TILE * 128 + bn * 128 + ((bc ^ (bn & 7)) << 4);
     for (int s = 0; s < SH_STAGES - 1; ++s) issue(lo + s, s);
     int slot = 0;
@@ -297,34 +270,39 @@ __global__ void __launch_bounds__(SH_THREADS) k_lora_shrink(const ShrinkArgs p) 
         cp_async_wait_group<SH_STAGES - 2>();
         __syncthreads();
         issue(s + SH_STAGES - 1, slot == 0 ? SH_STAGES - 1 : slot - 1);
-        const uint32_t st = ring + slot * STAGE;
-        uint32_t b[RC / 16][4];
+        if (m0 < count) {
 #pragma unroll
-        for (int i = 0; i < RC / 16; ++i) ldsm4(b[i], st + boff + i * 2048);
-#pragma unroll
-        for (int mt = 0; mt < LR_TILE / 16; ++mt)
-            if (16 * mt < count) {
-                uint32_t x[4];
-                ldsm4(x, st + aoff + mt * 2048);
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t st = ring + slot * STAGE + h * HALF;
+                uint32_t x[2][4];
+                ldsm4(x[0], st + aoff);
+                if (m0 + 16 < count) ldsm4(x[1], st + aoff + 2048);
 #pragma unroll
                 for (int i = 0; i < RC / 16; ++i) {
-                    mma_16x8x16<BF>(acc[mt][2 * i], x, b[i][0], b[i][1]);
-                    mma_16x8x16<BF>(acc[mt][2 * i + 1], x, b[i][2], b[i][3]);
+                    uint32_t b[4];
+                    ldsm4(b, st + boff + i * 2048);
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt)
+                        if (mt == 0 || m0 + 16 < count) {
+                            mma_16x8x16<BF>(acc[mt][2 * i], x[mt], b[0], b[1]);
+                            mma_16x8x16<BF>(acc[mt][2 * i + 1], x[mt], b[2], b[3]);
+                        }
                 }
             }
+        }
         slot = slot + 1 == SH_STAGES ? 0 : slot + 1;
     }
     cp_async_wait_all();
     __syncthreads();
 
-    // ---- partial sums: [warp][token][RC], then over the warps into the first
+    // ---- partial sums: [k16 warp][token][RC], then over those warps into the first
     float* part = reinterpret_cast<float*>(sm);
     const int g = lane >> 2, t4 = lane & 3;
 #pragma unroll
-    for (int mt = 0; mt < LR_TILE / 16; ++mt)
+    for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
         for (int i = 0; i < RC / 8; ++i) {
-            float* d = part + (warp * LR_TILE + 16 * mt + g) * RC + 8 * i + 2 * t4;
+            float* d = part + (wk * LR_TILE + m0 + 16 * mt + g) * RC + 8 * i + 2 * t4;
             *reinterpret_cast<float2*>(d) = make_float2(acc[mt][i][0], acc[mt][i][1]);
             *reinterpret_cast<float2*>(d + 8 * RC) = make_float2(acc[mt][i][2], acc[mt][i][3]);
         }
@@ -333,7 +311,7 @@ __global__ void __launch_bounds__(SH_THREADS) k_lora_shrink(const ShrinkArgs p) 
     for (int i = tid; i < count * (RC / 4); i += SH_THREADS) {
         float4 v = part4[i];
 #pragma unroll
-        for (int w = 1; w < SH_THREADS / 32; ++w) v = add4(v, part4[w * LR_TILE * (RC / 4) + i]);
+        for (int w = 1; w < 4; ++w) v = add4(v, part4[w * LR_TILE * (RC / 4) + i]);
         part4[i] = v;
     }
     cluster_sync();
@@ -352,272 +330,550 @@ __global__ void __launch_bounds__(SH_THREADS) k_lora_shrink(const ShrinkArgs p) 
         v.y = col + 1 < live ? __fmul_rn(v.y, scale) : 0.f;
         v.z = col + 2 < live ? __fmul_rn(v.z, scale) : 0.f;
         v.w = col + 3 < live ? __fmul_rn(v.w, scale) : 0.f;
-        if (r0 + col < p.r) put_t(p, start + row, r0 + col, v);
+        if (r0 + col < p.r) *reinterpret_cast<float4*>(p.T + static_cast<int64_t>(start + row) * p.r + r0 + col) = v;
     }
     cluster_sync();   // the partial sums stay until every CTA has read them
 }
 
 // ---------------------------------------------------------------------- expand
 struct ExpandArgs {
-    const void* T;
+    const float* T;
     const uint16_t* B;
     const int32_t *order, *tiles, *ranks;
     const void* base;
     void* Y;
     int64_t ldb, ldy;
-    int M, N, n, r;
+    int M, N, n, r, ntiles;
+    int blocks, depth;   // k_lora_expand: column blocks of a CTA, blocks of base rows in shared memory
 };
 
-// Eight consecutive outputs as loaded
-template <int YT>
-struct Out8 {
-    uint4 q[YT == HQ_F32 ? 2 : 1];
+// What a CTA of the kernels below works on; a bad tile has no tokens
+struct Tile {
+    int a, start, count, live;
 };
 
-template <int YT>
-__device__ __forceinline__ void ex_widen(const Out8<YT>& o, float (&v)[8]) {
-    if constexpr (YT == HQ_F32) {
-        const uint32_t t[8] = {o.q[0].x, o.q[0].y, o.q[0].z, o.q[0].w, o.q[1].x, o.q[1].y, o.q[1].z, o.q[1].w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(t[e]);
-    } else {
-        const uint32_t t[4] = {o.q[0].x, o.q[0].y, o.q[0].z, o.q[0].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if constexpr (YT == HQ_BF16) {
-                v[2 * e] = __uint_as_float(t[e] << 16);
-                v[2 * e + 1] = __uint_as_float(t[e] & 0xFFFF0000u);
-            } else {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&t[e]));
-                v[2 * e] = f.x;
-                v[2 * e + 1] = f.y;
-            }
-        }
-    }
+__device__ __forceinline__ Tile tile_of(const ExpandArgs& p, int i) {
+    Tile t;
+    t.a = p.tiles[3 * i];
+    t.start = p.tiles[3 * i + 1];
+    t.count = p.tiles[3 * i + 2];
+    if (t.count <= 0 || t.count > LR_TILE || t.start < 0 || t.start > p.M - t.count || t.a >= p.n) t.count = 0;
+    t.live = 0;
+    if (t.count > 0 && t.a >= 0) t.live = p.ranks != nullptr ? min(max(p.ranks[t.a], 0), p.r) : p.r;
+    return t;
 }
 
 template <int YT>
-__device__ __forceinline__ void ex_store8(void* p, int64_t i, const float (&v)[8]) {
-    if constexpr (YT == HQ_F32) {
-        float4* s = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-        s[0] = make_float4(v[0], v[1], v[2], v[3]);
-        s[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-        uint32_t t[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if constexpr (YT == HQ_BF16) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-                t[e] = *reinterpret_cast<const uint32_t*>(&b);
-            } else {
-                const __half2 b = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
-                t[e] = *reinterpret_cast<const uint32_t*>(&b);
-            }
-        }
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = make_uint4(t[0], t[1], t[2], t[3]);
+constexpr int out_bytes = YT == HQ_F32 ? 4 : 2;
+
+__device__ __forceinline__ float2 widen16(bool bf, uint32_t w) {
+    return bf ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u))
+              : __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+__device__ __forceinline__ uint32_t narrow16(bool bf, float a, float b) {
+    if (bf) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The tile's rows of Y are its rows of base (or zero): tokens without an adapter
+template <int YT>
+__device__ void copy_rows(const ExpandArgs& p, const Tile& t, int col0, int cols) {
+    if (p.base == p.Y) return;   // in place
+    constexpr int PER = 16 / out_bytes<YT>;
+    const int vecs = (min(cols, p.N - col0)) / PER;   // N is a multiple of 8
+    for (int i = threadIdx.x; i < t.count * vecs; i += blockDim.x) {
+        const int m = p.order[t.start + i / vecs], col = col0 + i % vecs * PER;
+        if (m < 0 || m >= p.M) continue;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (p.base != nullptr)
+            v = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.base) + (m * p.ldb + col) * out_bytes<YT>);
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.Y) + (m * p.ldy + col) * out_bytes<YT>) = v;
     }
 }
 
-constexpr int EX_WARPS = 4;
-constexpr int EX_COLS = 64 * EX_WARPS;
+// Few tokens per tile (decode): bound by the latency of its chain of loads and
+// by reading B once, so plain fp32 adds without staging or hand-over.  A thread
+// has two neighbouring columns; t is the same for the whole CTA (a broadcast
+// load); four tokens at a time share B's values in registers.
+constexpr int FEW_THREADS = 128;
+constexpr int FEW_COLS = 2 * FEW_THREADS;
 
-// A warp takes 64 output columns of a tile.  The product t B^T runs on the
-// bf16 MMA with t as two bf16 terms (16-bit Y: 2^-18 of t, far below Y's own
-// rounding) or three (fp32 Y), and an fp16 B as its two exact bf16 terms; the
-// fp16 MMA would not hold the range of t, and tf32 has a quarter of the rate.
-// Both index orders an MMA leaves open are chosen for the loads: within a chunk
-// of R rank positions lane t of a quad holds the R/4 consecutive ones from
-// R/4 t (vector loads of B and of t), and column c of the i-th of four n8
-// tiles is column 8 (c / 2) + 2 i + c % 2 of 32, which leaves each lane 8
-// consecutive outputs of a row, one 16-byte access of base and of Y.
-template <bool BF, int YT, int R, bool MULTI>
-__global__ void __launch_bounds__(EX_WARPS * 32) k_lora_expand(const ExpandArgs p) {
-    constexpr int KS = R / 16;               // k16 steps of a chunk
-    constexpr int BT = BF ? 1 : 2;           // terms of B
-    constexpr int TT = YT == HQ_F32 ? 3 : 2; // terms of t
-    extern __shared__ __align__(128) uint8_t sm[];   // t: [term][64][trow], then the base slots
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-    const int n0 = (blockIdx.x * EX_WARPS + warp) * 64;
-    const int a = p.tiles[3 * blockIdx.y], start = p.tiles[3 * blockIdx.y + 1], count = p.tiles[3 * blockIdx.y + 2];
-    const bool ok = count > 0 && count <= LR_TILE && start >= 0 && start <= p.M - count && a < p.n;
-    int live = 0;
-    if (ok && a >= 0) live = p.ranks != nullptr ? min(max(p.ranks[a], 0), p.r) : p.r;
-
-    uint32_t b[BT][2][4][KS][2];   // term, 32 columns, n8 tile, k16 step, register
+template <bool BF, int YT>
+__global__ void __launch_bounds__(FEW_THREADS) k_lora_expand_few(const ExpandArgs p) {
+    const Tile t = tile_of(p, blockIdx.y);
+    const int col = blockIdx.x * FEW_COLS + 2 * threadIdx.x;
+    const bool on = col < p.N;
+    const uint16_t* brow = p.B + (static_cast<int64_t>(t.a) * p.N + col) * p.r;
+    uint4 b[2][2];   // column, eight of sixteen rank positions
     auto load_b = [&](int c) {
 #pragma unroll
-        for (int w = 0; w < 2; ++w)
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int nn = n0 + 32 * w + 8 * (g >> 1) + 2 * i + (g & 1);
-                const int j0 = c * R + R / 4 * t4;
-                uint32_t v[KS * 2];
+            for (int e = 0; e < 2; ++e)
+                b[k][e] = on && c + 8 * e < t.live ? __ldg(reinterpret_cast<const uint4*>(brow + k * p.r + c + 8 * e))
+                                                   : make_uint4(0u, 0u, 0u, 0u);
+    };
+    int m[4];
+    float y[4][2];
+    auto load_base = [&](int i0) {
 #pragma unroll
-                for (int e = 0; e < KS * 2; ++e) v[e] = 0u;
-                if (nn < p.N) {
-                    const uint16_t* s = p.B + (static_cast<int64_t>(a) * p.N + nn) * p.r + j0;
-                    if constexpr (R == 16) {
-                        if (j0 < live) {
-                            const uint2 q = __ldg(reinterpret_cast<const uint2*>(s));
-                            v[0] = q.x; v[1] = q.y;
-                        }
-                    } else {
+        for (int i = 0; i < 4; ++i) {
+            m[i] = i0 + i < t.count ? p.order[t.start + i0 + i] : -1;
+            if (m[i] >= p.M) m[i] = -1;
+        }
 #pragma unroll
-                        for (int e = 0; e < KS / 2; ++e)
-                            if (j0 + 8 * e < live) {
-                                const uint4 q = __ldg(reinterpret_cast<const uint4*>(s) + e);
-                                v[4 * e] = q.x; v[4 * e + 1] = q.y; v[4 * e + 2] = q.z; v[4 * e + 3] = q.w;
-                            }
-                    }
+        for (int i = 0; i < 4; ++i) {
+            y[i][0] = y[i][1] = 0.f;
+            if (m[i] >= 0 && on && p.base != nullptr) {
+                const uint8_t* s = static_cast<const uint8_t*>(p.base) + (m[i] * p.ldb + col) * out_bytes<YT>;
+                const float2 v = YT == HQ_F32 ? *reinterpret_cast<const float2*>(s)
+                                              : widen16(YT == HQ_BF16, *reinterpret_cast<const uint32_t*>(s));
+                y[i][0] = v.x;
+                y[i][1] = v.y;
+            }
+        }
+    };
+    if (t.live > 0) {
+        load_base(0);
+        load_b(0);
+    }
+    griddep_wait();   // t is complete
+    if (t.live == 0) {
+        copy_rows<YT>(p, t, blockIdx.x * FEW_COLS, FEW_COLS);
+        return;
+    }
+    for (int i0 = 0; i0 < t.count; i0 += 4) {
+        if (i0 > 0) load_base(i0);
+        float acc[4][2] = {};
+        for (int c = 0; c < t.live; c += 16) {
+            if (i0 > 0 || c > 0) load_b(c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {   // four rank positions
+                if (c + 4 * e >= t.live) break;
+                float w[2][4];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint4 q = b[k][e >> 1];
+                    const float2 lo = widen16(BF, e & 1 ? q.z : q.x), hi = widen16(BF, e & 1 ? q.w : q.y);
+                    w[k][0] = lo.x; w[k][1] = lo.y; w[k][2] = hi.x; w[k][3] = hi.y;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)   // past the adapter's rank B is not read as a number
+                        if (c + 4 * e + u >= t.live) w[k][u] = 0.f;
                 }
 #pragma unroll
-                for (int e = 0; e < KS * 2; ++e) {
-                    // past the adapter's rank B is not read as a number
-                    if (j0 + 2 * e + 1 >= live) v[e] = j0 + 2 * e < live ? v[e] & 0xFFFFu : 0u;
-                    if constexpr (BF) {
-                        b[0][w][i][e / 2][e & 1] = v[e];
-                    } else {
-                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[e]));
-                        const float h0 = bf16_near(f.x), h1 = bf16_near(f.y);
-                        b[0][w][i][e / 2][e & 1] = bf16x2_of(h0, h1);
-                        b[BT - 1][w][i][e / 2][e & 1] = bf16x2_of(rest_of(f.x, h0), rest_of(f.y, h1));
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    if (i0 + i >= t.count) break;
+                    const float4 v =
+                        *reinterpret_cast<const float4*>(p.T + static_cast<int64_t>(t.start + i0 + i) * p.r + c + 4 * e);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        acc[i][k] = __fmaf_rn(v.w, w[k][3], __fmaf_rn(v.z, w[k][2], __fmaf_rn(v.y, w[k][1],
+                                              __fmaf_rn(v.x, w[k][0], acc[i][k]))));
                 }
             }
-    };
-    // this lane's base rows, on their way to slots of its own before t is awaited
-    const int rp = (p.r + R - 1) / R * R, trow = 2 * rp + 8;   // bytes of a staged row of t
-    uint8_t* slots = sm + TT * LR_TILE * trow + (warp * 32 + lane) * 16;
-    constexpr int PIECES = YT == HQ_F32 ? 2 : 1;
-    constexpr int SLOT = EX_WARPS * 32 * 16;   // from one piece of a lane to its next
-    int m[LR_TILE / 16][2];
+        }
 #pragma unroll
-    for (int mt = 0; mt < LR_TILE / 16; ++mt)
+        for (int i = 0; i < 4; ++i)
+            if (m[i] >= 0 && on) {
+                const float v0 = __fadd_rn(y[i][0], acc[i][0]), v1 = __fadd_rn(y[i][1], acc[i][1]);
+                uint8_t* d = static_cast<uint8_t*>(p.Y) + (m[i] * p.ldy + col) * out_bytes<YT>;
+                if constexpr (YT == HQ_F32)
+                    *reinterpret_cast<float2*>(d) = make_float2(v0, v1);
+                else
+                    *reinterpret_cast<uint32_t*>(d) = narrow16(YT == HQ_BF16, v0, v1);
+            }
+    }
+}
+
+// Whole tiles (prompts): t of two tiles (128 tokens) and blocks of 64 rows of B
+// are operands of tcgen05.mma (kind::f16, 128 x 64, fp32 accumulators in tensor
+// memory), so that the warps are left with what HBM sees: base in, Y out.
+//  * t enters as 16-bit terms: with bf16 B two bf16 terms for a 16-bit Y (2^-18
+//    of t, far below Y's rounding) and three for an fp32 Y; with fp16 B two
+//    fp16 terms (2^-22) of the row scaled by a power of two to below 2^14.
+//  * operands are K-major rows of 128 bytes (64 rank positions) in the 128-byte
+//    swizzle; rows of B are staged in the order that makes MMA column 8 i +
+//    2 t + e of each 32 the output column 8 t + 2 i + e: a lane of the
+//    16x256b accumulator layout then holds 8 consecutive outputs of a row.
+//  * the next two blocks' B and the next `depth` blocks' base rows (in slots
+//    that only their lane uses) are on their way (cp.async) while a block is
+//    multiplied and stored; two CTAs per SM cover each other's waits.
+// Two neighbouring tiles of one adapter are taken together; others one after
+// the other.
+// A ninth warp issues the products and waits for them: one thread that issues
+// between its own stores held up the other warps (1300 of 3600 cycles a block).
+constexpr int EX_THREADS = 256;                 // those that copy and store
+constexpr int EX_ROWS = 2 * LR_TILE;            // tokens of a product
+constexpr int EX_NB = 64;                       // columns of a block
+constexpr uint64_t EX_LIMIT_NS = 2000000000ull;
+
+__host__ __device__ constexpr int ex_terms(bool bf, int yt) { return bf && yt == HQ_F32 ? 3 : 2; }
+// bytes of shared memory: t, two blocks of B, base (`depth` blocks), row scales
+__host__ __device__ constexpr int ex_smem(bool bf, int yt, int atoms, int depth) {
+    return 1024 + ex_terms(bf, yt) * atoms * EX_ROWS * 128 + 2 * atoms * EX_NB * 128 +
+           depth * EX_ROWS * EX_NB * (yt == HQ_F32 ? 4 : 2) + EX_ROWS * 4;
+}
+
+// D[tmem] (+)= A[smem] B[smem]^T, 16-bit floats, fp32 accumulators, one CTA
+__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// One thread of a converged warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
+// RK: rank up to 16, 32, 64 (one row of 128 bytes of B and t) or above (64 rank
+// positions per atom, several atoms)
+template <bool BF, int YT, int RK>
+__global__ void __launch_bounds__(EX_THREADS + 32, 2) k_lora_expand(const ExpandArgs p) {
+    constexpr int SH = RK == 16 ? 1 : RK == 32 ? 2 : 3;   // log2 of the chunks per row of B that a pass of the threads takes
+    constexpr int TT = ex_terms(BF, YT);
+    constexpr int ES = out_bytes<YT>;
+    constexpr int PIECES = YT == HQ_F32 ? 2 : 1;
+    constexpr int BASE = EX_THREADS * 4 * 16 * PIECES;   // base slots of a block
+    constexpr int TATOM = EX_ROWS * 128, BATOM = EX_NB * 128;
+    constexpr uint32_t IDESC = (1u << 4) | ((BF ? 1u : 0u) << 7) | ((BF ? 1u : 0u) << 10) |
+                               (static_cast<uint32_t>(EX_NB >> 3) << 17) | (static_cast<uint32_t>(EX_ROWS >> 4) << 24);
+    extern __shared__ uint8_t dyn[];
+    __shared__ uint64_t bar_mem;
+    __shared__ uint32_t tmem_mem;
+    uint8_t* sm = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    const bool mma_warp = warp == EX_THREADS / 32;
+    const int quarter = warp & 3, c0 = 32 * (warp >> 2);   // rows 32 quarter .., columns c0 .. c0 + 31 of a block
+    const int blk0 = blockIdx.x * p.blocks, blk1 = min(blk0 + p.blocks, (p.N + EX_NB - 1) / EX_NB);
+    const int atoms = RK <= 64 ? 1 : (p.r + 63) / 64;
+    uint8_t* tbuf = sm;
+    uint8_t* bbuf = tbuf + TT * atoms * TATOM;
+    uint8_t* slots = bbuf + 2 * atoms * BATOM;
+    float* unscale = reinterpret_cast<float*>(slots + p.depth * BASE);
+    const uint32_t bar = smem_u32(&bar_mem);
+    // Tile i takes tile i + 1 along if they are the 2 k-th and the 2 k + 1-st of one
+    // adapter (only an adapter's last tile is not full)
+    const int ti = blockIdx.y;
+    const Tile t = tile_of(p, ti);
+    if (t.live == 0) {   // the same for the whole CTA
+        griddep_wait();
+        copy_rows<YT>(p, t, blk0 * EX_NB, (blk1 - blk0) * EX_NB);
+        return;
+    }
+    int before = 0;
+    for (int i = ti - 1 - tid; i >= 0; i -= EX_THREADS + 32) before ^= p.tiles[3 * i] == t.a;
+    if (__syncthreads_count(before) & 1) {
+        griddep_wait();
+        return;
+    }
+    int rows = t.count;
+    if (rows == LR_TILE && ti + 1 < p.ntiles) {
+        const Tile n = tile_of(p, ti + 1);
+        if (n.a == t.a && n.count > 0 && n.start == t.start + rows) rows += n.count;
+    }
+    if (mma_warp) {
+        tmem_alloc(smem_u32(&tmem_mem), 2 * EX_NB);
+        tmem_relinquish();
+    }
+    if (tid == 0) {
+        mbar_init(bar, 1);
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = tmem_mem;
+
+    // Row l of a block of B goes to row (l & ~31) + f(l & 31) of the operand, f(l) =
+    // 4 (l & 6) + 2 (l / 8) + (l & 1).  This thread's chunk of rows l0, l0 + LS, ...
+    constexpr int LS = EX_THREADS >> SH < EX_NB ? EX_THREADS >> SH : EX_NB, LN = EX_NB / LS;
+    const int chunk = tid & ((1 << SH) - 1), l0 = tid >> SH;
+    auto b_row = [](int l) { return (l & ~31) + ((l & 6) << 2) + (((l & 31) >> 3) << 1) + (l & 1); };
+    uint32_t boff[LN];
+#pragma unroll
+    for (int k = 0; k < LN; ++k) {
+        const int row = b_row(l0 + LS * k);
+        boff[k] = row * 128 + ((chunk ^ (row & 7)) << 4);
+    }
+
+    const int steps = (t.live + 15) / 16;   // k16 steps
+    if (mma_warp) {
+        // the product of block blk: t and B of shared memory into half blk & 1 of the accumulators
+        const uint64_t td = sw128_kmajor_desc(smem_u32(tbuf)), bd = sw128_kmajor_desc(smem_u32(bbuf));
+        griddep_wait();
+        uint32_t phase = 0;
+        bool lost = false;   // a wait gave up
+        for (int blk = blk0; blk <= blk1; ++blk) {
+            tc_fence_before();
+            lost = __syncthreads_or(lost);   // B of this block is there, the block before it is in the accumulators
+            if (lost || blk == blk1) break;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint32_t d = tm + (blk & 1) * EX_NB;
+                const uint64_t b = bd + static_cast<uint32_t>((blk & 1) * atoms * (BATOM >> 4));
+#pragma unroll
+                for (int e = TT - 1; e >= 0; --e) {   // small terms first
+                    if constexpr (RK <= 64) {
+#pragma unroll
+                        for (int s = 0; s < RK / 16; ++s)
+                            if (s < steps)
+                                mma_f16_ss(d, td + static_cast<uint32_t>(e * (TATOM >> 4) + 2 * s), b + 2u * s, IDESC,
+                                           e < TT - 1 || s > 0);
+                    } else {
+                        for (int s = 0; s < steps; ++s)
+                            mma_f16_ss(d, td + static_cast<uint32_t>((e * atoms + (s >> 2)) * (TATOM >> 4) + 2 * (s & 3)),
+                                       b + static_cast<uint32_t>((s >> 2) * (BATOM >> 4) + 2 * (s & 3)), IDESC,
+                                       e < TT - 1 || s > 0);
+                    }
+                }
+                tc_commit(bar);
+            }
+            __syncwarp();
+            lost = !mbar_wait(bar, phase, EX_LIMIT_NS);
+            phase ^= 1u;
+        }
+        __syncthreads();
+        tmem_dealloc(tm, 2 * EX_NB);
+        return;
+    }
+    int m[2][2];                            // this lane's rows 32 quarter + 16 f + 8 h + g
+    const uint8_t* ysrc[2][2];
+    uint8_t* ydst[2][2];
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int i = 16 * mt + 8 * h + g;
-            m[mt][h] = ok && i < count ? p.order[start + i] : -1;
-            if (m[mt][h] >= p.M) m[mt][h] = -1;
+            const int i = 32 * quarter + 16 * f + 8 * h + g;
+            m[f][h] = i < rows ? p.order[t.start + i] : -1;
+            if (m[f][h] >= p.M) m[f][h] = -1;
+            const int64_t col = static_cast<int64_t>(blk0) * EX_NB + c0 + 8 * t4;
+            const int64_t row = max(m[f][h], 0);
+            ysrc[f][h] = p.base != nullptr && m[f][h] >= 0
+                             ? static_cast<const uint8_t*>(p.base) + (row * p.ldb + col) * ES
+                             : nullptr;
+            ydst[f][h] = static_cast<uint8_t*>(p.Y) + (row * p.ldy + col) * ES;
         }
-    const bool keep = !ok || (live == 0 && p.base == p.Y);   // nothing to do: in place the rows stay as they are
-    if (p.base != nullptr && !keep) {
+    // the next block to copy, of B and of base: pointers that move on block by block
+    const uint16_t* bsrc =
+        p.B + (static_cast<int64_t>(t.a) * p.N + static_cast<int64_t>(blk0) * EX_NB + l0) * p.r + 8 * chunk;
+    int bleft = l0 < EX_NB ? p.N - blk0 * EX_NB - l0 : 0;   // this thread's rows in bounds: LS k < bleft
+    int bblk = blk0;
+    auto load_b = [&]() {
+        if (bblk < blk1) {
+            const uint32_t bd = smem_u32(bbuf) + (bblk & 1) * atoms * BATOM;
+#pragma unroll 1
+            for (int at = 0; at < atoms; ++at) {
+                const int j = 64 * at + 8 * chunk;   // rank position of the chunk
+                if (j < 16 * steps && l0 < EX_NB) {
+                    const uint16_t* src = bsrc + 64 * at;
 #pragma unroll
-        for (int mt = 0; mt < LR_TILE / 16; ++mt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const int col = n0 + 32 * w + 8 * t4;
-                    if (m[mt][h] >= 0 && col < p.N) {
-                        const uint8_t* src = static_cast<const uint8_t*>(p.base) + (m[mt][h] * p.ldb + col) * (PIECES * 2);
-#pragma unroll
-                        for (int e = 0; e < PIECES; ++e)
-                            cp_async16(smem_u32(slots + (((mt * 2 + h) * 2 + w) * PIECES + e) * SLOT), src + 16 * e);
+                    for (int k = 0; k < LN; ++k) {
+                        if (j < t.live && LS * k < bleft)
+                            cp_async16(bd + at * BATOM + boff[k], src);
+                        else
+                            cp_async16_z(bd + at * BATOM + boff[k], p.B, 0);
+                        src += static_cast<int64_t>(LS) * p.r;
                     }
                 }
-    }
-    if (!MULTI && live > 0) load_b(0);
-    griddep_wait();   // t is complete
-    if (live > 0) {   // the same for the whole CTA
-        const int64_t plane = static_cast<int64_t>(p.M) * p.r;
-        const int per = rp / 4;   // groups of four rank positions
-        for (int i = threadIdx.x; i < count * per; i += EX_WARPS * 32) {
-            const int row = i / per, j = i % per * 4;
-            const int64_t at = static_cast<int64_t>(start + row) * p.r + j;
-            uint8_t* dst = sm + row * trow + 2 * j;
-            if (j >= p.r) {
+            }
+            bsrc += static_cast<int64_t>(EX_NB) * p.r;
+            bleft -= EX_NB;
+            ++bblk;
+        }
+    };
+    // the last chunk of an adapter whose rank is no multiple of 8: what lies behind
+    // the rank is not read as a number (each thread mends what it copied)
+    auto mend = [&](int blk) {
+        const int j0 = t.live & ~7;
+        if ((t.live & 7) == 0 || chunk != ((j0 & 63) >> 3) || l0 >= EX_NB) return;
+        uint8_t* bd = bbuf + ((blk & 1) * atoms + (j0 >> 6)) * BATOM;
 #pragma unroll
-                for (int e = 0; e < TT; ++e) *reinterpret_cast<uint2*>(dst + e * LR_TILE * trow) = make_uint2(0u, 0u);
-            } else if constexpr (YT == HQ_F32) {
-                const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(p.T) + at);
-                float v[4] = {f.x, f.y, f.z, f.w};
+        for (int k = 0; k < LN; ++k) {
+            uint16_t* d = reinterpret_cast<uint16_t*>(bd + boff[k]);
+            for (int e = t.live & 7; e < 8; ++e) d[e] = 0;
+        }
+    };
+    const uint32_t slot0 = smem_u32(slots) + tid * 16;
+    int yleft = p.N - blk0 * EX_NB - c0 - 8 * t4;
+    auto load_base = [&](bool more, int slot) {
+        if (more) {
+            const uint32_t sd = slot0 + slot * BASE;
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (ysrc[f][h] != nullptr) {
+                        if (yleft > 0) {
+#pragma unroll
+                            for (int e = 0; e < PIECES; ++e)
+                                cp_async16(sd + ((f * 2 + h) * PIECES + e) * EX_THREADS * 16, ysrc[f][h] + 16 * e);
+                        }
+                        ysrc[f][h] += EX_NB * ES;
+                    }
+            yleft -= EX_NB;
+        }
+    };
+    load_b();
+    load_base(true, 0);
+    cp_async_commit();
+    load_b();
+    cp_async_commit();
+    for (int k = 1; k < p.depth; ++k) load_base(blk0 + k < blk1, k);
+    cp_async_commit();
+    griddep_wait();   // t is complete
+    {   // t in 16-bit terms: two threads per row take alternate chunks of 8 positions
+        const int row = tid >> 1;
+        const float* src = p.T + static_cast<int64_t>(t.start + row) * p.r;
+        float scale = 1.f;
+        if constexpr (!BF) {
+            float top = 0.f;
+            if (row < rows)
+                for (int c = tid & 1; 8 * c < t.live; c += 2)
+#pragma unroll
+                    for (int e = 0; e < 8; e += 4) {
+                        const float4 v = *reinterpret_cast<const float4*>(src + 8 * c + e);
+                        top = fmaxf(top, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+                    }
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            // 2^(13 - e) for top in [2^e, 2^(e+1)); e >= -100 keeps it finite
+            const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
+            if (top > 0.f && top < INFINITY) scale = __uint_as_float(static_cast<uint32_t>(127 + 13 - e) << 23);
+            if ((tid & 1) == 0) unscale[row] = __fdiv_rn(1.f, scale);   // a power of two: exact
+        }
+        if (row < rows)
+            for (int c = tid & 1; c < 2 * steps; c += 2) {
+                float v[8] = {};
+                if (8 * c < p.r) {
+                    const float4 a = *reinterpret_cast<const float4*>(src + 8 * c);
+                    const float4 b = *reinterpret_cast<const float4*>(src + 8 * c + 4);
+                    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+                    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+                }
+                if constexpr (!BF) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] = __fmul_rn(v[k], scale);
+                }
 #pragma unroll
                 for (int e = 0; e < TT; ++e) {
-                    const float q[4] = {bf16_near(v[0]), bf16_near(v[1]), bf16_near(v[2]), bf16_near(v[3])};
-                    *reinterpret_cast<uint2*>(dst + e * LR_TILE * trow) =
-                        make_uint2(bf16x2_of(q[0], q[1]), bf16x2_of(q[2], q[3]));
+                    uint32_t w[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) v[k] = rest_of(v[k], q[k]);
+                    for (int k = 0; k < 4; ++k) {
+                        w[k] = narrow16(BF, v[2 * k], v[2 * k + 1]);
+                        const float2 f = widen16(BF, w[k]);
+                        // the rest; none where the term is not finite
+                        v[2 * k] = fabsf(f.x) < INFINITY ? __fsub_rn(v[2 * k], f.x) : 0.f;
+                        v[2 * k + 1] = fabsf(f.y) < INFINITY ? __fsub_rn(v[2 * k + 1], f.y) : 0.f;
+                    }
+                    *reinterpret_cast<uint4*>(tbuf + (e * atoms + (c >> 3)) * TATOM + row * 128 +
+                                              (((c & 7) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-            } else {
-#pragma unroll
-                for (int e = 0; e < TT; ++e)
-                    cp_async8(smem_u32(dst + e * LR_TILE * trow), static_cast<const uint16_t*>(p.T) + e * plane + at);
             }
+    }
+    // Block b + 1 is multiplied while block b is stored.  Copy groups in order: B of
+    // b + 2 (over the B just multiplied), then the base rows of b + depth (over
+    // those just used); the product of b + 1 needs all but the last of them.
+    cp_async_wait_group<2>();
+    mend(blk0);
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads_or(0);
+    float us[2][2] = {{1.f, 1.f}, {1.f, 1.f}};
+    if constexpr (!BF) {
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) us[f][h] = unscale[32 * quarter + 16 * f + 8 * h + g];
+    }
+    int left = p.N - blk0 * EX_NB - c0 - 8 * t4;
+    int slot = 0;
+    for (int blk = blk0; blk < blk1; ++blk) {
+        if (p.depth > 1 || blk == blk0)
+            cp_async_wait_group<1>();
+        else
+            cp_async_wait_all();
+        if (blk + 1 < blk1) {
+            mend(blk + 1);
+            fence_proxy_async_smem();
         }
+        tc_fence_before();
+        if (__syncthreads_or(0)) break;   // the product of this block is done (or was given up)
+        load_b();
+        cp_async_commit();
+        if (32 * quarter < rows) {
+            tc_fence_after();
+            const uint8_t* sd = slots + slot * BASE + tid * 16;
+            uint32_t acc[2][16];
+            const uint32_t at = tm + (static_cast<uint32_t>(32 * quarter) << 16) + (blk & 1) * EX_NB + c0;
+            tmem_ld_16x256b_x4(at, acc[0]);
+            tmem_ld_16x256b_x4(at + (16u << 16), acc[1]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (m[f][h] < 0 || left <= 0) continue;
+#pragma unroll
+                    for (int e = 0; e < PIECES; ++e) {
+                        uint32_t w[4] = {0u, 0u, 0u, 0u};
+                        if (p.base != nullptr) {
+                            const uint4 y = *reinterpret_cast<const uint4*>(
+                                sd + ((f * 2 + h) * PIECES + e) * EX_THREADS * 16);
+                            w[0] = y.x; w[1] = y.y; w[2] = y.z; w[3] = y.w;
+                        }
+                        constexpr int PER = YT == HQ_F32 ? 1 : 2;   // outputs per word
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int o = (4 * e + k) * PER;   // output 2 i + c (of 8) is acc[4 i + 2 h + c]
+                            float v0 = __uint_as_float(acc[f][4 * (o / 2) + 2 * h + (o & 1)]);
+                            if constexpr (!BF) v0 = __fmul_rn(v0, us[f][h]);
+                            if constexpr (YT == HQ_F32) {
+                                w[k] = __float_as_uint(__fadd_rn(__uint_as_float(w[k]), v0));
+                            } else {
+                                float v1 = __uint_as_float(acc[f][4 * (o / 2) + 2 * h + 1]);
+                                if constexpr (!BF) v1 = __fmul_rn(v1, us[f][h]);
+                                const float2 y = widen16(YT == HQ_BF16, w[k]);
+                                w[k] = narrow16(YT == HQ_BF16, __fadd_rn(y.x, v0), __fadd_rn(y.y, v1));
+                            }
+                        }
+                        reinterpret_cast<uint4*>(ydst[f][h])[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    ydst[f][h] += EX_NB * ES;
+                }
+            load_base(blk + p.depth < blk1, slot);
+        }
+        cp_async_commit();
+        slot = slot + 1 == p.depth ? 0 : slot + 1;
+        left -= EX_NB;
     }
     cp_async_wait_all();
-    __syncthreads();
-    if (keep) return;
-#pragma unroll
-    for (int mt = 0; mt < LR_TILE / 16; ++mt) {
-        if (16 * mt >= count) break;
-        float acc[2][4][4];
-#pragma unroll
-        for (int w = 0; w < 2; ++w)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[w][i][e] = 0.f;
-        for (int c = 0; c * R < live; ++c) {
-            if (MULTI) load_b(c);
-            // small terms first; the product of both last terms is left out
-#pragma unroll
-            for (int e = TT - 1; e >= 0; --e)
-#pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    const uint8_t* src = sm + (e * LR_TILE + 16 * mt + g) * trow + 2 * (c * R + R / 4 * t4 + 4 * s);
-                    const uint2 q0 = *reinterpret_cast<const uint2*>(src);
-                    const uint2 q1 = *reinterpret_cast<const uint2*>(src + 8 * trow);
-                    const uint32_t t[4] = {q0.x, q1.x, q0.y, q1.y};
-#pragma unroll
-                    for (int f = BT - 1; f >= 0; --f)
-                        if (e + f < TT)
-#pragma unroll
-                            for (int w = 0; w < 2; ++w)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    mma_16x8x16<true>(acc[w][i], t, b[f][w][i][s][0], b[f][w][i][s][1]);
-                }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                const int col = n0 + 32 * w + 8 * t4;
-                if (m[mt][h] >= 0 && col < p.N) {
-                    float v[8] = {};
-                    if (p.base != nullptr) {
-                        Out8<YT> y;
-#pragma unroll
-                        for (int e = 0; e < PIECES; ++e)
-                            y.q[e] = *reinterpret_cast<const uint4*>(slots + (((mt * 2 + h) * 2 + w) * PIECES + e) * SLOT);
-                        ex_widen<YT>(y, v);
-                    }
-                    if (live > 0) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            v[2 * i] = __fadd_rn(v[2 * i], acc[w][i][2 * h]);
-                            v[2 * i + 1] = __fadd_rn(v[2 * i + 1], acc[w][i][2 * h + 1]);
-                        }
-                    }
-                    ex_store8<YT>(p.Y, m[mt][h] * p.ldy + col, v);
-                }
-            }
-    }
+    tc_fence_before();
+    __syncthreads();   // the accumulators may go
 }
 
 bool lr_al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 template <bool BF, int RC>
 hq_status launch_shrink(const ShrinkArgs& a, int tiles, cudaStream_t st) {
-    constexpr int ring = SH_STAGES * (LR_TILE + RC) * 128, part = SH_THREADS / 32 * LR_TILE * RC * 4;
+    constexpr int ring = SH_STAGES * (LR_TILE + RC) * 256, part = 4 * LR_TILE * RC * 4;
     constexpr int smem = ring > part ? ring : part;
     auto kern = k_lora_shrink<BF, RC>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return HQ_ERR_CUDA;
-    // K is cut as far as one wave of CTAs (two per SM) goes
-    const int z = (a.r + RC - 1) / RC;
-    const int cl = tiles * z <= 37 ? 8 : tiles * z <= 74 ? 4 : tiles * z <= 148 ? 2 : 1;
+    // K is cut as far as the GPU holds all CTAs at once
+    const int z = (a.r + RC - 1) / RC, slots = 148 * (RC == 64 ? 2 : 3);
+    int cl = SH_MAX_CL;
+    while (cl > 1 && static_cast<int64_t>(tiles) * z * cl > slots) cl /= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(cl, tiles, z);
     cfg.blockDim = dim3(SH_THREADS);
@@ -633,16 +889,9 @@ hq_status launch_shrink(const ShrinkArgs& a, int tiles, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
 }
 
-template <bool BF, int YT, int R, bool MULTI>
-hq_status launch_expand_r(const ExpandArgs& a, int tiles, cudaStream_t st) {
-    const int rp = (a.r + R - 1) / R * R;
-    const int smem = (YT == HQ_F32 ? 3 : 2) * LR_TILE * (2 * rp + 8) + EX_WARPS * 32 * 16 * 16 * (YT == HQ_F32 ? 2 : 1);
-    auto kern = k_lora_expand<BF, YT, R, MULTI>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return HQ_ERR_CUDA;
+template <bool BF, int YT>
+hq_status launch_expand(ExpandArgs a, int tiles, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((a.N + EX_COLS - 1) / EX_COLS, tiles);
-    cfg.blockDim = dim3(EX_WARPS * 32);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     // may start while k_lora_shrink runs; it waits for that grid's completion
     cudaLaunchAttribute attr[1];
@@ -650,19 +899,35 @@ hq_status launch_expand_r(const ExpandArgs& a, int tiles, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
-}
-
-// B's fragments stay in registers for a whole tile where the rank fits: 64
-// positions of a 16-bit B used as it is, 32 where B has two terms or t three
-template <bool BF, int YT>
-hq_status launch_expand(const ExpandArgs& a, int tiles, cudaStream_t st) {
-    if (a.r <= 16) return launch_expand_r<BF, YT, 16, false>(a, tiles, st);
-    if (a.r <= 32) return launch_expand_r<BF, YT, 32, false>(a, tiles, st);
-    if constexpr (BF && YT != HQ_F32) {
-        if (a.r <= 64) return launch_expand_r<BF, YT, 64, false>(a, tiles, st);
+    const int atoms = (a.r + 63) / 64;
+    // tiles of few tokens, or (bf16 with fp32 Y above rank 192) too much for shared memory
+    if (a.M < 16 * tiles || ex_smem(BF, YT, atoms, 1) > 227 * 1024) {
+        cfg.gridDim = dim3((a.N + FEW_COLS - 1) / FEW_COLS, tiles);
+        cfg.blockDim = dim3(FEW_THREADS);
+        return cudaLaunchKernelEx(&cfg, k_lora_expand_few<BF, YT>, a) == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
     }
-    return launch_expand_r<BF, YT, 32, true>(a, tiles, st);
+    for (a.depth = 3; a.depth > 1 && ex_smem(BF, YT, atoms, a.depth) > 227 * 1024; --a.depth) {}
+    const int smem = ex_smem(BF, YT, atoms, a.depth);
+    auto kern = a.r <= 16   ? k_lora_expand<BF, YT, 16>
+                : a.r <= 32 ? k_lora_expand<BF, YT, 32>
+                : a.r <= 64 ? k_lora_expand<BF, YT, 64>
+                            : k_lora_expand<BF, YT, 256>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return HQ_ERR_CUDA;
+    // a CTA stages its tiles' t once for all its blocks of columns: as many CTAs as
+    // the GPU holds at once (two per SM), counting at most `heads` tiles that lead
+    // a pair; three rounds of smaller CTAs measured 2% (8192 x 28672) to 15%
+    // (2048 x 4096) slower
+    const int64_t nblk = (a.N + EX_NB - 1) / EX_NB;
+    const int heads = (tiles + (a.n < tiles ? a.n : tiles) + 1) / 2;
+    int64_t strips = 148 * 2 / heads;
+    strips = strips < 1 ? 1 : strips > nblk ? nblk : strips;
+    const int64_t per = (nblk + strips - 1) / strips;
+    a.blocks = static_cast<int>(per);
+    a.ntiles = tiles;
+    cfg.gridDim = dim3(static_cast<unsigned>((nblk + per - 1) / per), tiles);
+    cfg.blockDim = dim3(EX_THREADS + 32);
+    cfg.dynamicSmemBytes = smem;
+    return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
 }
 
 template <bool BF>
@@ -736,8 +1001,7 @@ extern "C" hq_status hq_lora_apply(const void* X, hq_dtype xt, int64_t M, int64_
     s.X = static_cast<const uint16_t*>(X);
     s.A = static_cast<const uint16_t*>(A);
     s.order = order; s.tiles = tiles; s.ranks = ranks; s.scales = scales;
-    s.T = workspace;
-    s.planes = yt == HQ_F32 ? 0 : 2;
+    s.T = static_cast<float*>(workspace);
     s.ldx = ld_x;
     s.M = static_cast<int>(M); s.K = static_cast<int>(K); s.n = static_cast<int>(n); s.r = r_max;
     ExpandArgs e = {};
