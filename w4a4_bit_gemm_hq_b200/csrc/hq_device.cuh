@@ -4,6 +4,7 @@
 // records a timeout in the device status word instead of spinning forever.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -26,6 +27,25 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
     uint64_t t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
+}
+
+// Host: allows `kern` up to kMaxDynSmem bytes of dynamic shared memory on the
+// current device, once per kernel and device (the call takes as long as a
+// small launch); `done` is a static of the caller, one per kernel.  Always the
+// same amount, so that calls from several threads cannot undo each other.
+constexpr int kMaxDynSmem = 226 * 1024;   // of 227 KB; the rest is for static shared memory
+struct SmemOptIn {
+    std::atomic<bool> dev[64] = {};
+};
+template <class Kern>
+inline bool allow_smem(SmemOptIn& done, Kern kern, int bytes) {
+    if (bytes <= 40 * 1024) return true;   // leaves room for static shared memory below 48 KB
+    int dev = 0;
+    if (bytes > kMaxDynSmem || cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev < 64 && done.dev[dev].load(std::memory_order_relaxed)) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynSmem) != cudaSuccess) return false;
+    if (dev < 64) done.dev[dev].store(true, std::memory_order_relaxed);
+    return true;
 }
 
 // ------------------------------------------------------------------ mbarrier

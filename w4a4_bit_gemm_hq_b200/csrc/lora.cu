@@ -869,7 +869,8 @@ hq_status launch_shrink(const ShrinkArgs& a, int tiles, cudaStream_t st) {
     constexpr int ring = SH_STAGES * (LR_TILE + RC) * 256, part = 4 * LR_TILE * RC * 4;
     constexpr int smem = ring > part ? ring : part;
     auto kern = k_lora_shrink<BF, RC>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return HQ_ERR_CUDA;
+    static SmemOptIn opt_in;
+    if (!allow_smem(opt_in, kern, smem)) return HQ_ERR_CUDA;
     // K is cut as far as the GPU holds all CTAs at once
     const int z = (a.r + RC - 1) / RC, slots = 148 * (RC == 64 ? 2 : 3);
     int cl = SH_MAX_CL;
@@ -901,18 +902,20 @@ hq_status launch_expand(ExpandArgs a, int tiles, cudaStream_t st) {
     cfg.numAttrs = 1;
     const int atoms = (a.r + 63) / 64;
     // tiles of few tokens, or (bf16 with fp32 Y above rank 192) too much for shared memory
-    if (a.M < 16 * tiles || ex_smem(BF, YT, atoms, 1) > 227 * 1024) {
+    if (a.M < 16 * tiles || ex_smem(BF, YT, atoms, 1) > kMaxDynSmem) {
         cfg.gridDim = dim3((a.N + FEW_COLS - 1) / FEW_COLS, tiles);
         cfg.blockDim = dim3(FEW_THREADS);
         return cudaLaunchKernelEx(&cfg, k_lora_expand_few<BF, YT>, a) == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
     }
-    for (a.depth = 3; a.depth > 1 && ex_smem(BF, YT, atoms, a.depth) > 227 * 1024; --a.depth) {}
+    for (a.depth = 3; a.depth > 1 && ex_smem(BF, YT, atoms, a.depth) > kMaxDynSmem; --a.depth) {}
     const int smem = ex_smem(BF, YT, atoms, a.depth);
-    auto kern = a.r <= 16   ? k_lora_expand<BF, YT, 16>
-                : a.r <= 32 ? k_lora_expand<BF, YT, 32>
-                : a.r <= 64 ? k_lora_expand<BF, YT, 64>
-                            : k_lora_expand<BF, YT, 256>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return HQ_ERR_CUDA;
+    const int rk = a.r <= 16 ? 0 : a.r <= 32 ? 1 : a.r <= 64 ? 2 : 3;
+    auto kern = rk == 0   ? k_lora_expand<BF, YT, 16>
+                : rk == 1 ? k_lora_expand<BF, YT, 32>
+                : rk == 2 ? k_lora_expand<BF, YT, 64>
+                          : k_lora_expand<BF, YT, 256>;
+    static SmemOptIn opt_in[4];
+    if (!allow_smem(opt_in[rk], kern, smem)) return HQ_ERR_CUDA;
     // a CTA stages its tiles' t once for all its blocks of columns: as many CTAs as
     // the GPU holds at once (two per SM), counting at most `heads` tiles that lead
     // a pair; three rounds of smaller CTAs measured 2% (8192 x 28672) to 15%
@@ -965,8 +968,8 @@ extern "C" hq_status hq_lora_plan(const int32_t* ids, int64_t M, int64_t n, int3
     const int smem = (W * nb + 2 * (nb + 1)) * 4;
     // a thread per bucket and one for the totals
     const int threads = 32 * W > nb + 1 ? 32 * W : (nb + 1 + 31) / 32 * 32;
-    if (cudaFuncSetAttribute(k_lora_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return HQ_ERR_CUDA;
+    static SmemOptIn opt_in;
+    if (!allow_smem(opt_in, k_lora_plan, smem)) return HQ_ERR_CUDA;
     k_lora_plan<<<1, threads, smem, static_cast<cudaStream_t>(stream)>>>(
         ids, static_cast<int>(M), static_cast<int>(n), W, run, order, tiles, static_cast<int>(hq_lora_max_tiles(M, n)));
     return cudaGetLastError() == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;

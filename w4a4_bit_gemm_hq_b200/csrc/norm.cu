@@ -408,9 +408,8 @@ hq_status nm_launch(const NormArgs& a, cudaStream_t st) {
     const int threads = (a.K + NM_SPAN - 1) / NM_SPAN * 32;
     const size_t shm = a.group > NM_SPAN ? static_cast<size_t>(threads) * 32 * sizeof(float) : 0;
     auto run = [&](auto kern) -> hq_status {
-        if (shm > 40 * 1024 &&
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shm)) != cudaSuccess)
-            return HQ_ERR_CUDA;
+        static SmemOptIn opt_in;   // of the one kernel of this instance that takes any (BITS != 0)
+        if (!allow_smem(opt_in, kern, static_cast<int>(shm))) return HQ_ERR_CUDA;
         kern<<<static_cast<unsigned>(a.M), threads, shm, st>>>(a);
         return cudaGetLastError() == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
     };

@@ -358,48 +358,67 @@ def hq_mxfp4_linear(Xq, sx, Wq, sw, Y=None, accumulate=False):
 
 # ------------------------------------------------- between two layers of a decoder
 # These calls check devices, types and shapes themselves (ValueError) and run
-# on the device of their first tensor, on its current stream.
+# on the device of their first tensor, on its current stream.  A single-token
+# call takes a few microseconds on the GPU, less than plain Python marshalling:
+# the checks are one comparison each, pointers and the stream are passed as
+# integers, and the device is switched only where it is not the current one.
 
-def _rows(t, name, like, M, K, dtype=None):
+def _device(t, name):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("%s must be on a CUDA device" % name)
+    return dev
+
+
+def _rows(t, name, dev, M, K, dtype):
     """Row stride in elements of an [M, K] tensor whose rows are contiguous."""
-    if t.device != like.device or not t.is_cuda:
-        raise ValueError("%s must be on the CUDA device of the first argument" % name)
-    if t.dtype != (like.dtype if dtype is None else dtype):
-        raise ValueError("%s must be %s, not %s" % (name, like.dtype if dtype is None else dtype, t.dtype))
-    if t.shape != (M, K):
-        raise ValueError("%s must have the shape (%d, %d), not %s" % (name, M, K, tuple(t.shape)))
-    if K > 1 and M > 0 and t.stride(1) != 1:
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != (M, K):
+        raise ValueError("%s must be a %s tensor of shape (%d, %d) on the device of the first argument"
+                         % (name, dtype, M, K))
+    s0, s1 = t.stride()
+    if s1 != 1 and K > 1 and M > 0:
         raise ValueError("%s must have contiguous rows" % name)
     # the stride of a single row (or of none) says nothing
-    return t.stride(0) if M > 1 else max(K + 7 & ~7, t.stride(0) & ~7)
+    return s0 if M > 1 else max(K + 7 & ~7, s0 & ~7)
 
 
-def _vector(t, name, like, n, dtype):
-    if t.device != like.device or t.dtype != dtype or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor of %d entries on the device of the first argument"
-                         % (name, dtype, n))
-
-
-def _whole(t, name, like, shape, dtype):
-    if t.device != like.device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+def _whole(t, name, dev, shape, dtype):
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s on the device of the first argument"
                          % (name, dtype, tuple(shape)))
 
 
-def _norm_args(H, w, Y, w_post, gate, H_out, X, M, K):
+def _launch(dev, fn, where, *args):
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        raise HQError(status, where)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _norm_args(H, dev, w, Y, w_post, gate, H_out, X, M, K):
     """Checks shared by the two calls below; the row strides (H, Y, gate, H_out, X) and the weights' type."""
-    wt = w.dtype if w is not None else w_post.dtype if w_post is not None else H.dtype
-    for t, name in ((w, "w"), (w_post, "w_post")):
-        if t is not None:
-            _vector(t, name, H, K, wt)
+    dt = H.dtype
+    wt = w.dtype if w is not None else w_post.dtype if w_post is not None else dt
+    if w is not None:
+        _whole(w, "w", dev, (K,), wt)
+    if w_post is not None:
+        _whole(w_post, "w_post", dev, (K,), wt)
     ld_g = 0
     if gate is not None:
         if gate.dim() == 1:
-            _vector(gate, "gate", H, K, H.dtype)
+            _whole(gate, "gate", dev, (K,), dt)
         else:
-            ld_g = _rows(gate, "gate", H, M, K)
-    return (_rows(H, "H", H, M, K), 0 if Y is None else _rows(Y, "Y", H, M, K), ld_g,
-            0 if H_out is None else _rows(H_out, "H_out", H, M, K), 0 if X is None else _rows(X, "X", H, M, K), wt)
+            ld_g = _rows(gate, "gate", dev, M, K, dt)
+    return (_rows(H, "H", dev, M, K, dt), 0 if Y is None else _rows(Y, "Y", dev, M, K, dt), ld_g,
+            0 if H_out is None else _rows(H_out, "H_out", dev, M, K, dt),
+            0 if X is None else _rows(X, "X", dev, M, K, dt), dtype_code(wt))
 
 
 def _new_rows(like, M, K):
@@ -415,16 +434,15 @@ def hq_residual_norm(H, w, eps, Y=None, w_post=None, gate=None, alpha=1.0, w_off
     block's output Y, and its RMS norm with weights w (None: no second norm, X is
     None).  gate is [K] or [M, K]; w_offset is added to w and w_post.  H_out may
     be H (in place) and X may be Y; without Y there is no H_out unless one is given."""
+    dev = _device(H, "H")
     M, K = H.shape
     if Y is not None and H_out is None:
         H_out = _new_rows(H, M, K)
     if w is not None and X is None:
         X = _new_rows(H, M, K)
-    ld_h, ld_y, ld_g, ld_ho, ld_x, wt = _norm_args(H, w, Y, w_post, gate, H_out, X, M, K)
-    with torch.cuda.device(H.device):
-        check(lib.hq_residual_norm(ptr(H), ld_h, ptr(Y), ld_y, dtype_code(H.dtype), M, K, ptr(w_post), ptr(gate), ld_g,
-                                   alpha, ptr(w), dtype_code(wt), w_offset, eps, ptr(H_out), ld_ho, ptr(X), ld_x,
-                                   stream_handle()), "hq_residual_norm")
+    ld_h, ld_y, ld_g, ld_ho, ld_x, wt = _norm_args(H, dev, w, Y, w_post, gate, H_out, X, M, K)
+    _launch(dev, lib.hq_residual_norm, "hq_residual_norm", H.data_ptr(), ld_h, _at(Y), ld_y, dtype_code(H.dtype), M, K,
+            _at(w_post), _at(gate), ld_g, alpha, _at(w), wt, w_offset, eps, _at(H_out), ld_ho, _at(X), ld_x)
     return H_out, X
 
 
@@ -433,46 +451,51 @@ def hq_norm_rotate_quant(H, w, eps, group, H_signs=None, Y=None, gate=None, alph
     """(Xq, sx, H_out, X): hq_residual_norm (no norm after the block) with
     hq_rotate_quant (bits=4) or hq_rotate_quant8 (bits=8) in one pass; the
     normed rows X only with want_x or an X to write."""
+    dev = _device(H, "H")
     M, K = H.shape
     if Y is not None and H_out is None:
         H_out = _new_rows(H, M, K)
     if want_x and X is None:
         X = _new_rows(H, M, K)
     shape, dtype = ((M, K), torch.int8) if bits == 8 else ((M, K // 2), torch.uint8)
-    Xq = torch.empty(shape, dtype=dtype, device=H.device) if Xq is None else Xq
-    sx = torch.empty((M,), dtype=torch.float32, device=H.device) if sx is None else sx
-    _whole(Xq, "Xq", H, shape, dtype)
-    _vector(sx, "sx", H, M, torch.float32)
+    if Xq is None:
+        Xq = torch.empty(shape, dtype=dtype, device=H.device)
+    else:
+        _whole(Xq, "Xq", dev, shape, dtype)
+    if sx is None:
+        sx = torch.empty((M,), dtype=torch.float32, device=H.device)
+    else:
+        _whole(sx, "sx", dev, (M,), torch.float32)
     if H_signs is not None:
-        _vector(H_signs, "H_signs", H, group, torch.int8)
-    ld_h, ld_y, ld_g, ld_ho, ld_x, wt = _norm_args(H, w, Y, None, gate, H_out, X, M, K)
-    with torch.cuda.device(H.device):
-        check(lib.hq_norm_rotate_quant(ptr(H), ld_h, ptr(Y), ld_y, dtype_code(H.dtype), M, K, ptr(gate), ld_g, alpha,
-                                       ptr(w), dtype_code(wt), w_offset, eps, group, ptr(H_signs), bits, ptr(H_out),
-                                       ld_ho, ptr(X), ld_x, ptr(Xq), ptr(sx), stream_handle()),
-              "hq_norm_rotate_quant")
+        _whole(H_signs, "H_signs", dev, (group,), torch.int8)
+    ld_h, ld_y, ld_g, ld_ho, ld_x, wt = _norm_args(H, dev, w, Y, None, gate, H_out, X, M, K)
+    _launch(dev, lib.hq_norm_rotate_quant, "hq_norm_rotate_quant", H.data_ptr(), ld_h, _at(Y), ld_y,
+            dtype_code(H.dtype), M, K, _at(gate), ld_g, alpha, _at(w), wt, w_offset, eps, group, _at(H_signs), bits,
+            _at(H_out), ld_ho, _at(X), ld_x, Xq.data_ptr(), sx.data_ptr())
     return Xq, sx, H_out, X
 
 
 def hq_lora_max_tiles(M, n):
-    return int(lib.hq_lora_max_tiles(M, n))
+    return M // 64 + min(n + 1, M) if M > 0 and n >= 0 else 0     # as the C call
 
 
 def hq_lora_plan(ids, n, order=None, tiles=None):
     """(order int32 [M], tiles int32 [hq_lora_max_tiles(M, n), 3]): the tokens of a
     batch grouped by their adapter ids int32 [M] in [0, n), -1 for none.  One
     plan serves every adapted layer of the step."""
+    dev = _device(ids, "ids")
     M = ids.shape[0]
-    _vector(ids, "ids", ids, M, torch.int32)
+    _whole(ids, "ids", dev, (M,), torch.int32)
     rows = hq_lora_max_tiles(M, n)
-    order = torch.empty((M,), dtype=torch.int32, device=ids.device) if order is None else order
-    tiles = torch.empty((rows, 3), dtype=torch.int32, device=ids.device) if tiles is None else tiles
-    if not ids.is_cuda:
-        raise ValueError("ids must be on a CUDA device")
-    _vector(order, "order", ids, M, torch.int32)
-    _whole(tiles, "tiles", ids, (rows, 3), torch.int32)
-    with torch.cuda.device(ids.device):
-        check(lib.hq_lora_plan(ptr(ids), M, n, ptr(order), ptr(tiles), stream_handle()), "hq_lora_plan")
+    if order is None:
+        order = torch.empty((M,), dtype=torch.int32, device=ids.device)
+    else:
+        _whole(order, "order", dev, (M,), torch.int32)
+    if tiles is None:
+        tiles = torch.empty((rows, 3), dtype=torch.int32, device=ids.device)
+    else:
+        _whole(tiles, "tiles", dev, (rows, 3), torch.int32)
+    _launch(dev, lib.hq_lora_plan, "hq_lora_plan", ids.data_ptr(), M, n, order.data_ptr(), tiles.data_ptr())
     return order, tiles
 
 
@@ -485,30 +508,32 @@ def hq_lora_apply(X, A, B, order, tiles, ranks=None, scales=None, base=None, Y=N
     alone (zero if None) for a token without one.  A [n, r_max, K] and B
     [n, N, r_max] have X's type; order and tiles come from hq_lora_plan.  Y may be
     base (in place); it has base's type, or out_dtype (X's by default)."""
+    dev = _device(X, "X")
+    dt = X.dtype
     M, K = X.shape
-    n, r, N = A.shape[0], A.shape[1], B.shape[1]
+    n, r, _ = A.shape
+    N = B.shape[1]
     if Y is None:
-        dt = base.dtype if base is not None else X.dtype if out_dtype is None else out_dtype
-        Y = torch.empty((M, N), dtype=dt, device=X.device)
-    ld_x, ld_y = _rows(X, "X", X, M, K), _rows(Y, "Y", X, M, N, Y.dtype)
-    ld_b = 0 if base is None else _rows(base, "base", X, M, N, Y.dtype)
-    _whole(A, "A", X, (n, r, K), X.dtype)
-    _whole(B, "B", X, (n, N, r), X.dtype)
-    _vector(order, "order", X, M, torch.int32)
-    _whole(tiles, "tiles", X, (hq_lora_max_tiles(M, n), 3), torch.int32)
+        yt = base.dtype if base is not None else dt if out_dtype is None else out_dtype
+        Y = torch.empty((M, N), dtype=yt, device=X.device)
+    yt = Y.dtype
+    ld_x, ld_y = _rows(X, "X", dev, M, K, dt), _rows(Y, "Y", dev, M, N, yt)
+    ld_b = 0 if base is None else ld_y if base is Y else _rows(base, "base", dev, M, N, yt)
+    _whole(A, "A", dev, (n, r, K), dt)
+    _whole(B, "B", dev, (n, N, r), dt)
+    _whole(order, "order", dev, (M,), torch.int32)
+    _whole(tiles, "tiles", dev, (hq_lora_max_tiles(M, n), 3), torch.int32)
     if ranks is not None:
-        _vector(ranks, "ranks", X, n, torch.int32)
+        _whole(ranks, "ranks", dev, (n,), torch.int32)
     if scales is not None:
-        _vector(scales, "scales", X, n, torch.float32)
-    with torch.cuda.device(X.device):
-        if workspace is None:
-            workspace = torch.empty((M, r), dtype=torch.float32, device=X.device)
-        elif workspace.device != X.device or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the device of X")
-        check(lib.hq_lora_apply(ptr(X), dtype_code(X.dtype), M, K, ld_x, ptr(A), ptr(B), N, n, r, ptr(ranks),
-                                ptr(scales), ptr(order), ptr(tiles), ptr(base), ld_b, ptr(Y), dtype_code(Y.dtype), ld_y,
-                                ptr(workspace), workspace.numel() * workspace.element_size(), stream_handle()),
-              "hq_lora_apply")
+        _whole(scales, "scales", dev, (n,), torch.float32)
+    if workspace is None:
+        workspace = torch.empty((M, r), dtype=torch.float32, device=X.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the device of X")
+    _launch(dev, lib.hq_lora_apply, "hq_lora_apply", X.data_ptr(), dtype_code(dt), M, K, ld_x, A.data_ptr(),
+            B.data_ptr(), N, n, r, _at(ranks), _at(scales), order.data_ptr(), tiles.data_ptr(), _at(base), ld_b,
+            Y.data_ptr(), dtype_code(yt), ld_y, workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return Y
 
 
