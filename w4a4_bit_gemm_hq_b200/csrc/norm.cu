@@ -22,6 +22,8 @@
 // (8 bits for sensitive layers); the norm itself is the RMS norm of the Llama
 // layers whose shapes the pages quote.
 #include <cstdint>
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -48,23 +50,36 @@ struct NormArgs {
 template <int XT>
 constexpr int vec_len = XT == HQ_F32 ? 4 : 8;
 
-// n < vec_len values: the row ends inside the vector
+// Row m of a matrix: the same for the whole CTA, so that a vector's address is
+// one uniform base and a 32-bit offset
 template <int XT>
-__device__ __forceinline__ uint4 ld_vec(const void* p, int64_t i, int n) {
+__device__ __forceinline__ const uint8_t* row_of(const void* p, int64_t m, int64_t ld) {
+    return static_cast<const uint8_t*>(p) + m * ld * (XT == HQ_F32 ? 4 : 2);
+}
+template <int XT>
+__device__ __forceinline__ uint8_t* row_of(void* p, int64_t m, int64_t ld) {
+    return static_cast<uint8_t*>(p) + m * ld * (XT == HQ_F32 ? 4 : 2);
+}
+
+// The vector at byte `at` of a row, n of its values (TAIL: the row may end inside
+// the vector; otherwise it is whole or absent)
+template <int XT, bool TAIL>
+__device__ __forceinline__ uint4 ld_vec(const uint8_t* row, uint32_t at, int n) {
+    if (!TAIL || n == vec_len<XT>)
+        return n > 0 ? __ldg(reinterpret_cast<const uint4*>(row + at)) : make_uint4(0u, 0u, 0u, 0u);
+    uint32_t t[4] = {0u, 0u, 0u, 0u};
     if constexpr (XT == HQ_F32) {
-        const float* s = static_cast<const float*>(p) + i;
-        if (n == 4) return __ldg(reinterpret_cast<const uint4*>(s));
-        return make_uint4(n > 0 ? __float_as_uint(__ldg(s)) : 0u, n > 1 ? __float_as_uint(__ldg(s + 1)) : 0u,
-                          n > 2 ? __float_as_uint(__ldg(s + 2)) : 0u, 0u);
+        const float* s = reinterpret_cast<const float*>(row + at);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < n) t[e] = __float_as_uint(__ldg(s + e));
     } else {
-        const uint16_t* s = static_cast<const uint16_t*>(p) + i;
-        if (n == 8) return __ldg(reinterpret_cast<const uint4*>(s));
-        uint32_t t[4] = {0u, 0u, 0u, 0u};
+        const uint16_t* s = reinterpret_cast<const uint16_t*>(row + at);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             if (e < n) t[e / 2] |= static_cast<uint32_t>(__ldg(s + e)) << (16 * (e & 1));
-        return make_uint4(t[0], t[1], t[2], t[3]);
     }
+    return make_uint4(t[0], t[1], t[2], t[3]);
 }
 
 template <int XT>
@@ -103,27 +118,23 @@ __device__ __forceinline__ uint4 narrow(const float (&v)[vec_len<XT>]) {
     return make_uint4(t[0], t[1], t[2], t[3]);
 }
 
-template <int XT>
-__device__ __forceinline__ void st_vec(void* p, int64_t i, int n, const uint4& q) {
+template <int XT, bool TAIL>
+__device__ __forceinline__ void st_vec(uint8_t* row, uint32_t at, int n, const uint4& q) {
+    if (!TAIL || n == vec_len<XT>) {
+        if (n > 0) *reinterpret_cast<uint4*>(row + at) = q;
+        return;
+    }
     const uint32_t t[4] = {q.x, q.y, q.z, q.w};
     if constexpr (XT == HQ_F32) {
-        float* s = static_cast<float*>(p) + i;
-        if (n == 4) {
-            *reinterpret_cast<uint4*>(s) = q;
-        } else {
+        float* s = reinterpret_cast<float*>(row + at);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (e < n) s[e] = __uint_as_float(t[e]);
-        }
+        for (int e = 0; e < 4; ++e)
+            if (e < n) s[e] = __uint_as_float(t[e]);
     } else {
-        uint16_t* s = static_cast<uint16_t*>(p) + i;
-        if (n == 8) {
-            *reinterpret_cast<uint4*>(s) = q;
-        } else {
+        uint16_t* s = reinterpret_cast<uint16_t*>(row + at);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e < n) s[e] = static_cast<uint16_t>(t[e / 2] >> (16 * (e & 1)));
-        }
+        for (int e = 0; e < 8; ++e)
+            if (e < n) s[e] = static_cast<uint16_t>(t[e / 2] >> (16 * (e & 1)));
     }
 }
 
@@ -135,7 +146,7 @@ __device__ __forceinline__ void ld_weight(const void* w, int wt, int i, int n, f
 #pragma unroll
         for (int h = 0; h < V; h += 4) {
             float t[4];
-            widen<HQ_F32>(ld_vec<HQ_F32>(w, i + h, min(max(n - h, 0), 4)), t);
+            widen<HQ_F32>(ld_vec<HQ_F32, true>(static_cast<const uint8_t*>(w), 4u * (i + h), min(max(n - h, 0), 4)), t);
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[h + e] = t[e];
         }
@@ -175,10 +186,9 @@ struct RowReduce {
     // (sum of s, max of a) over the CTA
     __device__ __forceinline__ float2 operator()(float s, float a) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, s, o));
-            a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
-        }
+        for (int o = 16; o > 0; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, s, o));
+        // a is not negative: its bits are ordered as it is
+        a = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(a)));
         const int nw = blockDim.x >> 5;
         if (nw > 1) {
             if ((threadIdx.x & 31) == 0) buf[par][threadIdx.x >> 5] = make_float2(s, a);
@@ -201,107 +211,138 @@ __device__ __forceinline__ float inv_rms(float sum, int K, float eps) {
 }
 
 // ---------------------------------------------------------- without a quantiser
-// One CTA per row, NV vectors per thread, vector i of thread t at i * threads + t.
-// Bound by HBM: everything that a row needs (stream, block, gate, weights) is
-// requested before the first reduction, and a row is in registers from then on.
-template <int XT, int NV, bool POST, int MAXT>
-__global__ void __launch_bounds__(MAXT) k_residual_norm(const NormArgs a) {
+// A CTA walks rows m, m + grid, ...; NV vectors per thread, vector i of thread t
+// at i * threads + t.  Bound by HBM: the weights stay in registers as fp32 over
+// the CTA's rows (KEEP) and the next row is requested before this one is worked
+// on; rows whose registers do not allow both (fp32, very wide ones) do neither,
+// other CTAs cover their waits.  A row is in registers from its load to its stores.
+template <int XT, int NV, bool POST, bool KEEP, bool TAIL, int MAXT>
+__global__ void __launch_bounds__(MAXT, !KEEP && MAXT == 512 ? 2 : 1) k_residual_norm(const NormArgs a) {
     constexpr int V = vec_len<XT>;
     __shared__ float2 red[2][32];
-    const int64_t m = blockIdx.x;
     RowReduce reduce{red, 0};
-    int col[NV], n[NV];
-    uint4 rh[NV], ry[NV], rg[NV];
+    int n[NV];
+    uint32_t col[NV], at[NV];   // first channel of a vector, its byte
+    float wp[KEEP && POST ? NV : 1][V], wn[KEEP ? NV : 1][V];
+    struct Row {
+        uint4 h[NV], y[NV], g[NV];
+    } r[KEEP ? 2 : 1];
+    auto load = [&](int64_t m, Row& q) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) q.h[i] = ld_vec<XT, TAIL>(row_of<XT>(a.H, m, a.ldh), at[i], n[i]);
+        if (a.Y != nullptr) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) q.y[i] = ld_vec<XT, TAIL>(row_of<XT>(a.Y, m, a.ldy), at[i], n[i]);
+            if (a.gate != nullptr) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) q.g[i] = ld_vec<XT, TAIL>(row_of<XT>(a.gate, m, a.ldg), at[i], n[i]);
+            }
+        }
+    };
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         col[i] = (i * blockDim.x + threadIdx.x) * V;
-        n[i] = min(max(a.K - col[i], 0), V);
-        rh[i] = ld_vec<XT>(a.H, m * a.ldh + col[i], n[i]);
+        at[i] = col[i] * (16 / V);
+        n[i] = min(max(a.K - static_cast<int>(col[i]), 0), V);
     }
-    if (a.Y != nullptr) {
+    load(blockIdx.x, r[0]);
+    if constexpr (KEEP) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) ry[i] = ld_vec<XT>(a.Y, m * a.ldy + col[i], n[i]);
-        if (a.gate != nullptr) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) rg[i] = ld_vec<XT>(a.gate, m * a.ldg + col[i], n[i]);
+        for (int i = 0; i < NV; ++i) {
+            if constexpr (POST) ld_weight<V>(a.w_post, a.wt, col[i], n[i], a.off, wp[i]);
+            if (a.w != nullptr) ld_weight<V>(a.w, a.wt, col[i], n[i], a.off, wn[i]);
         }
-        float rstd = 1.f;
-        if constexpr (POST) {
+    }
+    for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
+        Row& q = r[0];
+        if constexpr (KEEP) {
+            if (m + gridDim.x < a.M) load(m + gridDim.x, r[1]);
+        }
+        if (a.Y != nullptr) {
+            float rstd = 1.f;
+            if constexpr (POST) {
+                float ss = 0.f;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    float y[V];
+                    widen<XT>(q.y[i], y);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) ss = __fmaf_rn(y[e], y[e], ss);
+                }
+                rstd = inv_rms(reduce(ss, 0.f).x, a.K, a.eps);
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float p[V], h[V];
+                widen<XT>(q.y[i], p);
+                widen<XT>(q.h[i], h);
+                if constexpr (POST) {
+                    if constexpr (!KEEP) ld_weight<V>(a.w_post, a.wt, col[i], n[i], a.off, wp[0]);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) p[e] = __fmul_rn(__fmul_rn(p[e], wp[KEEP ? i : 0][e]), rstd);
+                }
+                if (a.gate != nullptr) {
+                    float g[V];
+                    widen<XT>(q.g[i], g);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) p[e] = __fmul_rn(g[e], p[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < V; ++e) h[e] = __fadd_rn(h[e], __fmul_rn(a.alpha, p[e]));
+                q.h[i] = narrow<XT>(h);   // what the norm reads is the stored stream
+            }
+        }
+        if (a.Ho != nullptr) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) st_vec<XT, TAIL>(row_of<XT>(a.Ho, m, a.ldho), at[i], n[i], q.h[i]);
+        }
+        if (a.w != nullptr) {
             float ss = 0.f;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                float y[V];
-                widen<XT>(ry[i], y);
+                float h[V];
+                widen<XT>(q.h[i], h);
 #pragma unroll
-                for (int e = 0; e < V; ++e) ss = __fmaf_rn(y[e], y[e], ss);
+                for (int e = 0; e < V; ++e) ss = __fmaf_rn(h[e], h[e], ss);
             }
-            rstd = inv_rms(reduce(ss, 0.f).x, a.K, a.eps);
+            const float rstd = inv_rms(reduce(ss, 0.f).x, a.K, a.eps);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float h[V];
+                widen<XT>(q.h[i], h);
+                if constexpr (!KEEP) ld_weight<V>(a.w, a.wt, col[i], n[i], a.off, wn[0]);
+#pragma unroll
+                for (int e = 0; e < V; ++e) h[e] = __fmul_rn(__fmul_rn(h[e], wn[KEEP ? i : 0][e]), rstd);
+                st_vec<XT, TAIL>(row_of<XT>(a.X, m, a.ldx), at[i], n[i], narrow<XT>(h));
+            }
         }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float p[V], h[V];
-            widen<XT>(ry[i], p);
-            widen<XT>(rh[i], h);
-            if constexpr (POST) {
-                float w[V];
-                ld_weight<V>(a.w_post, a.wt, col[i], n[i], a.off, w);
-#pragma unroll
-                for (int e = 0; e < V; ++e) p[e] = __fmul_rn(__fmul_rn(p[e], w[e]), rstd);
-            }
-            if (a.gate != nullptr) {
-                float g[V];
-                widen<XT>(rg[i], g);
-#pragma unroll
-                for (int e = 0; e < V; ++e) p[e] = __fmul_rn(g[e], p[e]);
-            }
-#pragma unroll
-            for (int e = 0; e < V; ++e) h[e] = __fadd_rn(h[e], __fmul_rn(a.alpha, p[e]));
-            rh[i] = narrow<XT>(h);   // what the norm reads is the stored stream
-        }
-    }
-    if (a.Ho != nullptr) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) st_vec<XT>(a.Ho, m * a.ldho + col[i], n[i], rh[i]);
-    }
-    if (a.w == nullptr) return;   // no norm behind the block
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        float h[V];
-        widen<XT>(rh[i], h);
-#pragma unroll
-        for (int e = 0; e < V; ++e) ss = __fmaf_rn(h[e], h[e], ss);
-    }
-    const float rstd = inv_rms(reduce(ss, 0.f).x, a.K, a.eps);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        float h[V], w[V];
-        widen<XT>(rh[i], h);
-        ld_weight<V>(a.w, a.wt, col[i], n[i], a.off, w);
-#pragma unroll
-        for (int e = 0; e < V; ++e) h[e] = __fmul_rn(__fmul_rn(h[e], w[e]), rstd);
-        st_vec<XT>(a.X, m * a.ldx + col[i], n[i], narrow<XT>(h));
+        if constexpr (KEEP)
+            r[0] = r[1];
+        else if (m + gridDim.x < a.M)
+            load(m + gridDim.x, r[0]);
     }
 }
 
 // ------------------------------------------------------------- with a quantiser
-// One CTA per row; a warp takes 1024 consecutive channels, 32 per thread.  The
-// butterfly runs in registers between shared-memory transposes of the warp's
-// 1024 fp32 values (a shuffle per element and stage took 4 times the
-// shared-memory instructions):
-//   layout A: thread l holds channels 256 i + 8 l .. + 7, i = 0..3 (16-byte loads
-//             and stores, contiguous over the warp): stages 1, 2, 4
-//   layout B: thread l holds channels 256 (l / 8) + l % 8 + 8 k, k = 0..31: stages
-//             8 .. 128
-//   layout C: thread l holds channels l + 32 q + 256 i, q = 0..7, i = 0..3: stages
-//             256, 512 (groups above 256)
-//   groups of 2048 and 4096: the 2 or 4 warps of a group exchange the rest in
-//             layout C, value by value, through shared memory
-// and back to A for the codes.  Channel c of the warp's 1024 is stored at
-// c + 8 (c / 256), which makes A's and B's accesses conflict-free (A's 16-byte
-// writes two-way).  Only the row's reduction (and the exchange) need the CTA.
-constexpr int NQ_SPAN = 1024;
-constexpr int NQ_BUF = NQ_SPAN + 32;   // floats per warp
+// A CTA walks rows; a warp takes 1024 consecutive channels of a row, 32 per
+// thread.  The weights, with the offset added and the rotation's signs d on
+// them, are staged in shared memory as fp32 once per CTA (h (w d) is exactly
+// (h w) d), and the next row is requested before this one is rotated.  The
+// butterfly runs in registers between shared-memory transposes of the fp32
+// values (a shuffle per element and stage took 4 times the shared-memory
+// instructions):
+//   layout A: thread l of a warp holds channels 256 i + 8 l .. + 7, i = 0..3 (16-byte
+//             loads and stores, contiguous over the warp): stages 1, 2, 4
+//   layout B: channels 256 (l / 8) + l % 8 + 8 k, k = 0..31: stages 8 .. 128
+//   layout D: (groups above 256) thread t of the group's g/32 threads holds
+//             channels t + (g/32) q + 256 j, j = 0 .. g/256 - 1: stages 256 ..
+// and back to A for the codes.  Channel c of the row is stored at c + 4 (c / 32) +
+// 8 (c / 256), which makes the accesses of all layouts free of bank conflicts; the
+// weights lie in slots of 16 bytes that only their lane uses.
+// A and B stay within the warp; D of groups of 2048 and 4096 needs the CTA.
+__host__ __device__ constexpr int nq_at(int c) { return c + 4 * (c >> 5) + 8 * (c >> 8); }
+constexpr int NQ_SPAN = 1024;                 // channels of a warp
+constexpr int NQ_BUF = nq_at(NQ_SPAN);        // floats for them, 1184
 
 __device__ __forceinline__ float2 f2_add(float2 a, float2 b) {
     float2 r;
@@ -311,7 +352,20 @@ __device__ __forceinline__ float2 f2_add(float2 a, float2 b) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
-__device__ __forceinline__ float2 f2_sub(float2 a, float2 b) { return f2_add(a, make_float2(-b.x, -b.y)); }
+// a - b, as the exact b * -1 plus a
+__device__ __forceinline__ float2 f2_sub(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, n;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 n, {%6, %6};\n\t"
+        "fma.rn.f32x2 z, y, n, x;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(-1.0f));
+    return r;
+}
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+    float r;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 
 // (a, b) -> (a + b, a - b) for the pairs of v[] whose index differs in bit S
 template <int S>
@@ -335,60 +389,118 @@ __device__ __forceinline__ void stage(float (&v)[32]) {
     }
 }
 
-template <int XT, int BITS>
+// Stages 256 .. 128 J of a group of 256 J channels in layout D; `base` is the
+// group's place in shared memory, t the thread's number in the group
+template <int J>
+__device__ __forceinline__ void stages_d(float (&v)[32], float* base, int t) {
+    float* p = base + t + 4 * (t >> 5);
+#pragma unroll
+    for (int q = 0; q < 32 / J; ++q)
+#pragma unroll
+        for (int j = 0; j < J; ++j) v[q * J + j] = p[nq_at(8 * J * q) + nq_at(256) * j];   // g/32 = 8 J
+    stage<1>(v);
+    if constexpr (J > 2) stage<2>(v);
+    if constexpr (J > 4) stage<4>(v);
+    if constexpr (J > 8) stage<8>(v);
+#pragma unroll
+    for (int q = 0; q < 32 / J; ++q)
+#pragma unroll
+        for (int j = 0; j < J; ++j) p[nq_at(8 * J * q) + nq_at(256) * j] = v[q * J + j];
+}
+
+// FULL: rows of a multiple of 1024 channels, every vector is there
+template <int XT, int BITS, bool FULL>
 __global__ void __launch_bounds__(NM_MAXK / NQ_SPAN * 32) k_norm_quant(const NormArgs a) {
     __shared__ float2 red[2][32];
-    extern __shared__ __align__(16) float xch[];   // NQ_BUF per warp
+    extern __shared__ __align__(16) float dyn[];   // weights, then the row
     // the small-M GEMM may be launched early: it waits for this grid's
     // completion before it reads the codes
     asm volatile("griddepcontrol.launch_dependents;");
     if (blockIdx.x == 0 && threadIdx.x == 0 && a.d != nullptr && a.d[0] == -1) record_status(HQ_ERR_ARG);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col0 = warp * NQ_SPAN + lane * 8;
-    const int64_t m = blockIdx.x;
+    const uint32_t at0 = 2 * col0;
     const int G = a.group;
     RowReduce reduce{red, 0};
-    float* buf = xch + warp * NQ_BUF;
-
-    // ---- the residual stream after the block, v = h (w + off)
-    float v[32];
-    float ss = 0.f;
-    {
-        bool on[4];   // K is a multiple of 32: vectors are whole or absent
-        uint4 rh[4], ry[4];
+    float* row = dyn + (blockDim.x >> 5) * NQ_SPAN;
+    float* buf = row + warp * NQ_BUF;
+    float* wrow = dyn + warp * NQ_SPAN + 4 * lane;   // + 256 i + 128 h: weights of half h of vector i
+    bool on[4];   // K is a multiple of 32: vectors are whole or absent
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            on[i] = col0 + 256 * i < a.K;
-            rh[i] = on[i] ? ld_vec<XT>(a.H, m * a.ldh + col0 + 256 * i, 8) : make_uint4(0u, 0u, 0u, 0u);
-        }
+    for (int i = 0; i < 4; ++i) on[i] = FULL || col0 + 256 * i < a.K;
+
+    struct Row {
+        uint4 h[4], y[4];
+    } r;
+    auto load = [&](int64_t m, Row& q) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            q.h[i] = ld_vec<XT, false>(row_of<XT>(a.H, m, a.ldh), at0 + 512 * i, on[i]);
         if (a.Y != nullptr) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                ry[i] = on[i] ? ld_vec<XT>(a.Y, m * a.ldy + col0 + 256 * i, 8) : make_uint4(0u, 0u, 0u, 0u);
+                q.y[i] = ld_vec<XT, false>(row_of<XT>(a.Y, m, a.ldy), at0 + 512 * i, on[i]);
         }
+    };
+    load(blockIdx.x, r);
+    // weights of this lane's channels (each lane reads back what it wrote), and the
+    // signs of d, bit 8 i + e
+    uint32_t neg = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (on[i]) {
+            float w[8];
+            ld_weight<8>(a.w, a.wt, col0 + 256 * i, 8, a.off, w);
+            if (a.d != nullptr) {
+                const int8_t* d = a.d + ((col0 + 256 * i) & (G - 1));
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (d[e] == -1) {
+                        neg |= 1u << (8 * i + e);
+                        w[e] = -w[e];
+                    }
+            }
+            *reinterpret_cast<float4*>(wrow + 256 * i) = make_float4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<float4*>(wrow + 256 * i + 128) = make_float4(w[4], w[5], w[6], w[7]);
+        }
+    }
+    const int ia = 8 * lane + 4 * (lane >> 2);               // layout A: nq_at(8 l); + nq_at(256) i
+    const int ib = nq_at(256) * (lane >> 3) + (lane & 7);    // layout B: + nq_at(8 k)
+    float* gbase = nullptr;                                  // layout D: the group and the thread's number in it
+    int gt = 0;
+    if (G > 256) {
+        const int tg = G / 32;
+        gt = threadIdx.x & (tg - 1);
+        gbase = row + (threadIdx.x / tg) * ((G >> 8) * nq_at(256));
+    }
+
+    for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
+        // ---- the residual stream after the block, v = h (w + off) d
+        float v[32];
+        float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int col = col0 + 256 * i;
             float h[8];
-            widen<XT>(rh[i], h);
+            widen<XT>(r.h[i], h);
             if (a.Y != nullptr) {
                 float p[8];
-                widen<XT>(ry[i], p);
+                widen<XT>(r.y[i], p);
                 if (a.gate != nullptr && on[i]) {
                     float g[8];
-                    widen<XT>(ld_vec<XT>(a.gate, m * a.ldg + col, 8), g);
+                    widen<XT>(ld_vec<XT, false>(row_of<XT>(a.gate, m, a.ldg), at0 + 512 * i, 1), g);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) p[e] = __fmul_rn(g[e], p[e]);
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) h[e] = __fadd_rn(h[e], __fmul_rn(a.alpha, p[e]));
-                rh[i] = narrow<XT>(h);
-                widen<XT>(rh[i], h);   // what the norm reads is the stored stream
+                r.h[i] = narrow<XT>(h);
+                widen<XT>(r.h[i], h);   // what the norm reads is the stored stream
             }
-            if (a.Ho != nullptr && on[i]) st_vec<XT>(a.Ho, m * a.ldho + col, 8, rh[i]);
+            if (a.Ho != nullptr) st_vec<XT, false>(row_of<XT>(a.Ho, m, a.ldho), at0 + 512 * i, on[i], r.h[i]);
             if (on[i]) {
-                float w[8];
-                ld_weight<8>(a.w, a.wt, col, 8, a.off, w);
+                const float4 w0 = *reinterpret_cast<const float4*>(wrow + 256 * i);
+                const float4 w1 = *reinterpret_cast<const float4*>(wrow + 256 * i + 128);
+                const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     ss = __fmaf_rn(h[e], h[e], ss);
@@ -399,6 +511,7 @@ __global__ void __launch_bounds__(NM_MAXK / NQ_SPAN * 32) k_norm_quant(const Nor
                 for (int e = 0; e < 8; ++e) v[8 * i + e] = 0.f;
             }
         }
+        if (m + gridDim.x < a.M) load(m + gridDim.x, r);   // arrives while this row is rotated
         if (a.X != nullptr) {
             const float rstd = inv_rms(reduce(ss, 0.f).x, a.K, a.eps);
 #pragma unroll
@@ -406,142 +519,157 @@ __global__ void __launch_bounds__(NM_MAXK / NQ_SPAN * 32) k_norm_quant(const Nor
                 if (on[i]) {
                     float x[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(v[8 * i + e], rstd);
-                    st_vec<XT>(a.X, m * a.ldx + col0 + 256 * i, 8, narrow<XT>(x));
+                    for (int e = 0; e < 8; ++e)   // without the sign
+                        x[e] = __uint_as_float(__float_as_uint(__fmul_rn(v[8 * i + e], rstd)) ^
+                                               ((neg << (31 - 8 * i - e)) & 0x80000000u));
+                    st_vec<XT, false>(row_of<XT>(a.X, m, a.ldx), at0 + 512 * i, 1, narrow<XT>(x));
                 }
         }
-        if (a.d != nullptr) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int8_t* d = a.d + ((col0 + 256 * i) & (G - 1));
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[8 * i + e] = d[e] == -1 ? -v[8 * i + e] : v[8 * i + e];
-            }
-        }
-    }
-    // ---- butterfly, stages in ascending order
-    stage<1>(v);
-    stage<2>(v);
-    stage<4>(v);
-    const int ia = 8 * lane, ib = 264 * (lane >> 3) + (lane & 7);   // layouts A (+ 264 i), B (+ 8 k)
-    if (G > 8) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 8; e += 4)
-                *reinterpret_cast<float4*>(buf + ia + 264 * i + e) =
-                    make_float4(v[8 * i + e], v[8 * i + e + 1], v[8 * i + e + 2], v[8 * i + e + 3]);
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] = buf[ib + 8 * k];
+        // ---- butterfly, stages in ascending order
         stage<1>(v);
-        if (G > 16) stage<2>(v);
-        if (G > 32) stage<4>(v);
-        if (G > 64) stage<8>(v);
-        if (G > 128) stage<16>(v);
-        if (G > 256) {   // each thread writes where it read
+        stage<2>(v);
+        stage<4>(v);
+        float amax[4] = {0.f, 0.f, 0.f, 0.f};
+        if (G > 8) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) buf[ib + 8 * k] = v[k];
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; e += 4)
+                    *reinterpret_cast<float4*>(buf + ia + nq_at(256) * i + e) =
+                        make_float4(v[8 * i + e], v[8 * i + e + 1], v[8 * i + e + 2], v[8 * i + e + 3]);
             __syncwarp();
-            // layout C, element 4 q + i: channel lane + 32 q + 256 i
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = buf[lane + 32 * (k >> 2) + 264 * (k & 3)];
+            for (int k = 0; k < 32; ++k) v[k] = buf[ib + nq_at(8 * k)];
             stage<1>(v);
-            if (G > 512) stage<2>(v);
-            for (int s = 1; NQ_SPAN * s < G; s <<= 1) {   // partner warp
-                const float f = (warp & s) ? -1.f : 1.f;
-                const float* other = xch + (warp ^ s) * NQ_BUF;
-                if (s > 1) __syncthreads();   // the stage before has been read
+            if (G > 16) stage<2>(v);
+            if (G > 32) stage<4>(v);
+            if (G > 64) stage<8>(v);
+            if (G > 128) stage<16>(v);
+            // each thread writes where it read
 #pragma unroll
-                for (int k = 0; k < 32; ++k) buf[lane + 32 * (k >> 2) + 264 * (k & 3)] = v[k];
-                __syncthreads();
-                // the upper warp holds the second term: -own + partner
-#pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] = __fmaf_rn(v[k], f, other[lane + 32 * (k >> 2) + 264 * (k & 3)]);
+            for (int k = 0; k < 32; ++k) buf[ib + nq_at(8 * k)] = v[k];
+            if (G > 256) {
+                if (G > NQ_SPAN)
+                    __syncthreads();
+                else
+                    __syncwarp();
+                if (G == 512)
+                    stages_d<2>(v, gbase, gt);
+                else if (G == 1024)
+                    stages_d<4>(v, gbase, gt);
+                else if (G == 2048)
+                    stages_d<8>(v, gbase, gt);
+                else
+                    stages_d<16>(v, gbase, gt);
             }
         }
-    }
-    // ---- row scale; back to layout A
-    float amax = 0.f;
 #pragma unroll
-    for (int k = 0; k < 32; ++k) amax = fmaxf(amax, fabsf(v[k]));
-    if (G > NQ_SPAN) __syncthreads();   // the last exchange has been read
-    if (G > 256) {
+        for (int k = 0; k < 32; k += 2) amax[(k >> 1) & 3] = max3_abs(amax[(k >> 1) & 3], v[k], v[k + 1]);
+        // ---- row scale; back to layout A
+        const float2 t = reduce(ss, fmaxf(fmaxf(amax[0], amax[1]), fmaxf(amax[2], amax[3])));
+        if (G > 8) {
+            __syncwarp();   // one warp per row: the reduction has no barrier
 #pragma unroll
-        for (int k = 0; k < 32; ++k) buf[lane + 32 * (k >> 2) + 264 * (k & 3)] = v[k];
-    } else if (G > 8) {
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int k = 0; k < 32; ++k) buf[ib + 8 * k] = v[k];
-    }
-    const float2 t = reduce(ss, amax);
-    amax = t.y;
-    if (G > 8) {
-        __syncwarp();
+                for (int e = 0; e < 8; e += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(buf + ia + nq_at(256) * i + e);
+                    v[8 * i + e] = f.x; v[8 * i + e + 1] = f.y; v[8 * i + e + 2] = f.z; v[8 * i + e + 3] = f.w;
+                }
+        }
+        constexpr float LEVELS = BITS == 8 ? 127.0f : 7.0f;
+        const float inv = t.y == 0.f ? 0.f : __fdiv_rn(LEVELS, t.y);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) {
+            if (!on[i]) continue;
+            uint8_t* qrow = a.Xq + m * (BITS == 8 ? a.K : a.K / 2);
+            const uint32_t at = BITS == 8 ? col0 + 256 * i : (col0 + 256 * i) / 2;
+            // fl(u * inv) is at most LEVELS (1 + 2^-23): adding 1.5 * 2^23 (+ 8 for
+            // unsigned nibbles) rounds it to an integer, ties to even, whose bits end
+            // the sum.  The product is rounded on its own (a packed one would be
+            // merged with the sum).
+            constexpr float MAGIC = BITS == 8 ? 12582912.0f : 12582920.0f;
+            uint32_t c[8];
 #pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(buf + ia + 264 * i + e);
-                v[8 * i + e] = f.x; v[8 * i + e + 1] = f.y; v[8 * i + e + 2] = f.z; v[8 * i + e + 3] = f.w;
+            for (int e = 0; e < 8; e += 2) {
+                const float2 s = f2_add(make_float2(__fmul_rn(v[8 * i + e], inv), __fmul_rn(v[8 * i + e + 1], inv)),
+                                        make_float2(MAGIC, MAGIC));
+                c[e] = __float_as_uint(s.x);
+                c[e + 1] = __float_as_uint(s.y);
             }
-    }
-    constexpr float LEVELS = BITS == 8 ? 127.0f : 7.0f;
-    const float inv = amax == 0.f ? 0.f : __fdiv_rn(LEVELS, amax);
+            if constexpr (BITS == 8) {
+                const uint32_t lo = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+                const uint32_t hi = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
+                *reinterpret_cast<uint2*>(qrow + at) = make_uint2(lo, hi);
+            } else {
+                // the low byte of c + 16 c' is two nibbles q + 8; flipping their top bits
+                // makes them two's complement
+                uint32_t b[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (col0 + 256 * i >= a.K) continue;
-        const int64_t at = m * a.K + col0 + 256 * i;
-        // fl(u * inv) is at most LEVELS (1 + 2^-23): adding 1.5 * 2^23 rounds it
-        // to an integer, ties to even, whose two's complement bits end the sum
-        uint32_t c[8];
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-            const float2 r = f2_add(make_float2(__fmul_rn(v[8 * i + e], inv), __fmul_rn(v[8 * i + e + 1], inv)),
-                                    make_float2(12582912.0f, 12582912.0f));
-            c[e] = __float_as_uint(r.x);
-            c[e + 1] = __float_as_uint(r.y);
+                for (int e = 0; e < 4; ++e) b[e] = c[2 * e] + (c[2 * e + 1] << 4);
+                *reinterpret_cast<uint32_t*>(qrow + at) =
+                    __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410) ^ 0x88888888u;
+            }
         }
-        if constexpr (BITS == 8) {
-            const uint32_t lo = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
-            const uint32_t hi = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
-            *reinterpret_cast<uint2*>(a.Xq + at) = make_uint2(lo, hi);
-        } else {
-            uint32_t b = 0u;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) b |= (c[e] & 0xFu) << (4 * e);
-            *reinterpret_cast<uint32_t*>(a.Xq + at / 2) = b;
+        // a row with a NaN has a NaN scale, also where nothing else is left of it
+        if (threadIdx.x == 0) {
+            const float rstd = inv_rms(t.x, a.K, a.eps);
+            a.sx[m] = t.y == 0.f ? (rstd != rstd ? rstd : 0.f) : __fmul_rn(__fmul_rn(__fdiv_rn(t.y, LEVELS), a.cg), rstd);
         }
-    }
-    // a row with a NaN has a NaN scale, also where nothing else is left of it
-    if (threadIdx.x == 0) {
-        const float rstd = inv_rms(t.x, a.K, a.eps);
-        a.sx[m] = amax == 0.f ? (rstd != rstd ? rstd : 0.f) : __fmul_rn(__fmul_rn(__fdiv_rn(amax, LEVELS), a.cg), rstd);
     }
 }
 
 bool nm_al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool nm_type(int t) { return t == HQ_F16 || t == HQ_BF16 || t == HQ_F32; }
 
+// One CTA per row, or as many as the current device holds at once; 0 on an error
+template <class Kern>
+unsigned grid_for(Kern kern, int threads, int smem, int64_t M) {
+    if (M <= 128) return static_cast<unsigned>(M);   // the least that a device of this kind holds: no need to ask
+    int dev = 0, per_sm = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || per_sm < 1)
+        return 0;
+    const int64_t n = static_cast<int64_t>(per_sm) * sms;
+    return static_cast<unsigned>(n < M ? n : M);
+}
+
 template <int XT>
 hq_status launch_norm(const NormArgs& a, cudaStream_t st) {
-    constexpr int V = vec_len<XT>, NV = XT == HQ_F32 ? 4 : 2;
+    // vectors per thread in blocks of up to 512 threads, and in larger ones
+    constexpr int V = vec_len<XT>, NV = XT == HQ_F32 ? 3 : 2, NW = XT == HQ_F32 ? 4 : 2;
     const int vecs = (a.K + V - 1) / V;
-    const int threads = ((vecs + NV - 1) / NV + 31) / 32 * 32;   // at most 1024
-    // up to 512 threads have 128 registers each, which an fp32 row takes
-    auto kern = a.w_post != nullptr ? threads <= 512 ? k_residual_norm<XT, NV, true, 512> : k_residual_norm<XT, NV, true, 1024>
-                : threads <= 512    ? k_residual_norm<XT, NV, false, 512>
-                                    : k_residual_norm<XT, NV, false, 1024>;
-    kern<<<static_cast<unsigned>(a.M), threads, 0, st>>>(a);
+    const bool small = vecs <= 512 * NV;
+    const int nv = small ? NV : NW, threads = ((vecs + nv - 1) / nv + 31) / 32 * 32;   // at most 1024
+    // up to 512 threads have 128 registers each, enough to keep the weights
+    constexpr bool KEEP = XT != HQ_F32;
+    const bool tail = a.K % V != 0;
+    auto pick = [&](auto post) {
+        constexpr bool P = decltype(post)::value;
+        return small ? tail ? k_residual_norm<XT, NV, P, KEEP, true, 512> : k_residual_norm<XT, NV, P, KEEP, false, 512>
+               : tail ? k_residual_norm<XT, NW, P, false, true, 1024>
+                      : k_residual_norm<XT, NW, P, false, false, 1024>;
+    };
+    auto kern = a.w_post != nullptr ? pick(std::true_type{}) : pick(std::false_type{});
+    // rows of their own for CTAs that keep nothing from one to the next
+    const unsigned grid = KEEP && small ? grid_for(kern, threads, 0, a.M) : static_cast<unsigned>(a.M);
+    if (grid == 0) return HQ_ERR_CUDA;
+    kern<<<grid, threads, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
 }
 
 template <int XT, int BITS>
 hq_status launch_norm_quant(const NormArgs& a, cudaStream_t st) {
     const int warps = (a.K + NQ_SPAN - 1) / NQ_SPAN;
-    const int smem = warps * NQ_BUF * static_cast<int>(sizeof(float));
-    static SmemOptIn opt_in;
-    if (!allow_smem(opt_in, k_norm_quant<XT, BITS>, smem)) return HQ_ERR_CUDA;
-    k_norm_quant<XT, BITS><<<static_cast<unsigned>(a.M), 32 * warps, smem, st>>>(a);
+    const int smem = warps * (NQ_BUF + NQ_SPAN) * static_cast<int>(sizeof(float));
+    const bool full = a.K % NQ_SPAN == 0;
+    auto kern = full ? k_norm_quant<XT, BITS, true> : k_norm_quant<XT, BITS, false>;
+    static SmemOptIn opt_in[2];
+    if (!allow_smem(opt_in[full], kern, smem)) return HQ_ERR_CUDA;
+    const unsigned grid = grid_for(kern, 32 * warps, smem, a.M);
+    if (grid == 0) return HQ_ERR_CUDA;
+    kern<<<grid, 32 * warps, smem, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
 }
 
