@@ -26,47 +26,71 @@ constexpr int LR_MAX_ADAPTERS = 1022;   // the plan's CTA has a thread per bucke
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ------------------------------------------------------------------------ plan
-// One CTA: each warp takes a contiguous run of tokens.  Tokens are counted per
-// (warp, adapter) in shared memory, the counts scanned in (adapter, warp) order,
-// and the tokens placed in their order: the rank of a token among those of the
-// same adapter in its group of 32 comes from a warp match.  Bucket 0 holds the
-// tokens without an adapter.
+// A cluster of CTAs (one for short batches), each a contiguous run of tokens, and
+// each warp of a CTA a run of that.  Tokens are counted per (warp, adapter) in
+// shared memory, the counts scanned in (adapter, CTA, warp) order, and the tokens
+// placed in their order: the rank of a token among those of the same adapter in
+// its group of 32 comes from a warp match.  Bucket 0 holds the tokens without an
+// adapter.  Bound by the latency of these steps, not by its few bytes.
 constexpr int PL_THREADS = 1024;
+constexpr int PL_RUN = 4096;        // tokens of a CTA before another one is added
+constexpr int PL_MAX_CL = 8;
 
 __global__ void __launch_bounds__(PL_THREADS) k_lora_plan(const int32_t* __restrict__ ids, int M, int n, int W, int run,
                                                           int32_t* __restrict__ order, int32_t* __restrict__ tiles,
                                                           int max_tiles) {
-    extern __shared__ int32_t cnt[];   // [W][n + 1], then begin and first tile per bucket [2][n + 2]
+    extern __shared__ int32_t cnt[];   // [W][nb]; begin and first tile per bucket [2][nb + 1]; tokens per bucket [nb]
     __shared__ unsigned long long wsum[PL_THREADS / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = blockIdx.x, cl = gridDim.x;
     const int nb = n + 1;
     int32_t* begin = cnt + W * nb;
     int32_t* first = begin + nb + 1;
+    int32_t* mine = first + nb + 1;
     for (int i = tid; i < W * nb; i += blockDim.x) cnt[i] = 0;
     __syncthreads();
-    auto bucket = [&](int m) {
-        const int id = __ldg(ids + m);
-        if (id < -1 || id >= n) {
-            record_status(HQ_ERR_ARG);
-            return 0;
-        }
-        return id + 1;
-    };
-    const int lo = warp * run, hi = min(lo + run, M);
+    auto bucket = [&](int id) { return id < -1 || id >= n ? 0 : id + 1; };
+    const int lo = (rank * W + warp) * run, hi = min(lo + run, M);
+    bool bad = false;
     if (warp < W)
-        for (int m = lo + lane; m < hi; m += 32) atomicAdd(cnt + warp * nb + bucket(m), 1);
+        for (int m0 = lo; m0 < hi; m0 += 128) {   // four loads on their way at a time
+            int id[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) id[k] = m0 + 32 * k + lane < hi ? __ldg(ids + m0 + 32 * k + lane) : -1;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                bad |= id[k] < -1 || id[k] >= n;
+                if (m0 + 32 * k + lane < hi) atomicAdd(cnt + warp * nb + bucket(id[k]), 1);
+            }
+        }
+    if (bad) record_status(HQ_ERR_ARG);
     __syncthreads();
-    // thread b: bucket b's total over the warps, then (tokens, tiles) before it
+    // thread b: bucket b's tokens in this CTA, over its warps
     int total = 0;
-    if (tid < nb)
+    if (tid < nb) {
         for (int w = 0; w < W; ++w) {
             const int c = cnt[w * nb + tid];
             cnt[w * nb + tid] = total;
             total += c;
         }
-    const unsigned long long mine =
+        mine[tid] = total;
+    }
+    int ahead = 0;   // bucket b's tokens in the CTAs before this one
+    if (cl > 1) {
+        cluster_sync();
+        total = 0;
+        if (tid < nb)
+            for (int c = 0; c < cl; ++c) {
+                int32_t v;
+                asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(mine + tid), c)) : "memory");
+                if (c < rank) ahead += v;
+                total += v;
+            }
+    }
+    // (tokens, tiles) before bucket b
+    const unsigned long long own =
         (static_cast<unsigned long long>(total) << 32) | static_cast<unsigned>((total + LR_TILE - 1) / LR_TILE);
-    unsigned long long inc = mine;
+    unsigned long long inc = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const unsigned long long t = __shfl_up_sync(0xFFFFFFFFu, inc, o);
@@ -74,17 +98,35 @@ __global__ void __launch_bounds__(PL_THREADS) k_lora_plan(const int32_t* __restr
     }
     if (lane == 31) wsum[warp] = inc;
     __syncthreads();
-    unsigned long long before = inc - mine;
+    unsigned long long before = inc - own;
     for (int w = 0; w < warp; ++w) before += wsum[w];
     if (tid <= nb) {   // entry nb: the totals
         begin[tid] = static_cast<int32_t>(before >> 32);
         first[tid] = static_cast<int32_t>(before & 0xFFFFFFFFull);
     }
     if (tid < nb)
-        for (int w = 0; w < W; ++w) cnt[w * nb + tid] += static_cast<int32_t>(before >> 32);
+        for (int w = 0; w < W; ++w) cnt[w * nb + tid] += static_cast<int32_t>(before >> 32) + ahead;
     __syncthreads();
+    if (warp < W)
+        for (int m0 = lo; m0 < hi; m0 += 128) {
+            int b[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)   // lanes behind the end form a bucket of their own
+                b[k] = m0 + 32 * k + lane < hi ? bucket(__ldg(ids + m0 + 32 * k + lane)) : -1;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const unsigned same = __match_any_sync(0xFFFFFFFFu, b[k]);
+                const int at = b[k] >= 0 ? cnt[warp * nb + b[k]] : 0;
+                __syncwarp();
+                if (b[k] >= 0) {
+                    order[at + __popc(same & ((1u << lane) - 1u))] = m0 + 32 * k + lane;
+                    if (lane == __ffs(same) - 1) cnt[warp * nb + b[k]] = at + __popc(same);
+                }
+                __syncwarp();
+            }
+        }
     // tiles: the bucket of tile t is the last one whose first tile is <= t
-    for (int t = tid; t < max_tiles; t += blockDim.x) {
+    for (int t = rank * blockDim.x + tid; t < max_tiles; t += cl * blockDim.x) {
         int a = -1, s = 0, c = 0;
         if (t < first[nb]) {
             int l = 0, r = nb;
@@ -100,22 +142,7 @@ __global__ void __launch_bounds__(PL_THREADS) k_lora_plan(const int32_t* __restr
         tiles[3 * t + 1] = s;
         tiles[3 * t + 2] = c;
     }
-    if (warp < W)
-        for (int m0 = lo; m0 < hi; m0 += 32) {
-            const int m = m0 + lane;
-            const bool on = m < hi;
-            const unsigned act = __ballot_sync(0xFFFFFFFFu, on);
-            if (on) {
-                const int id = __ldg(ids + m);
-                const int b = (id < -1 || id >= n) ? 0 : id + 1;
-                const unsigned same = __match_any_sync(act, b);
-                const int at = cnt[warp * nb + b];
-                order[at + __popc(same & ((1u << lane) - 1u))] = m;
-                __syncwarp(act);
-                if (lane == __ffs(same) - 1) cnt[warp * nb + b] = at + __popc(same);
-            }
-            __syncwarp();
-        }
+    if (cl > 1) cluster_sync();   // the counts stay until every CTA has read them
 }
 
 // ---------------------------------------------------------------------- shrink
@@ -960,19 +987,33 @@ extern "C" hq_status hq_lora_plan(const int32_t* ids, int64_t M, int64_t n, int3
     if (n > LR_MAX_ADAPTERS || hq_lora_max_tiles(M, n) > 65535) return HQ_ERR_UNSUPPORTED;
     if (M == 0) return HQ_OK;
     if (!ids || !order || !tiles) return HQ_ERR_ARG;
-    // a warp per 32 tokens, as far as the counters of its own fit
+    int cl = 1;
+    while (cl < PL_MAX_CL && M > static_cast<int64_t>(PL_RUN) * cl) cl *= 2;
+    // a warp per 32 tokens, up to a full CTA
     const int nb = static_cast<int>(n) + 1;
-    int W = static_cast<int>((M + 31) / 32);
-    if (W > PL_THREADS / 32) W = PL_THREADS / 32;
-    const int run = static_cast<int>(((M + W - 1) / W + 31) / 32 * 32);
-    const int smem = (W * nb + 2 * (nb + 1)) * 4;
+    const int64_t per = (M + cl - 1) / cl;
+    const int W = static_cast<int>(per < PL_THREADS ? (per + 31) / 32 : PL_THREADS / 32);
+    const int run = static_cast<int>(((per + W - 1) / W + 31) / 32 * 32);
+    const int smem = (W * nb + 2 * (nb + 1) + nb) * 4;
     // a thread per bucket and one for the totals
     const int threads = 32 * W > nb + 1 ? 32 * W : (nb + 1 + 31) / 32 * 32;
     static SmemOptIn opt_in;
     if (!allow_smem(opt_in, k_lora_plan, smem)) return HQ_ERR_CUDA;
-    k_lora_plan<<<1, threads, smem, static_cast<cudaStream_t>(stream)>>>(
-        ids, static_cast<int>(M), static_cast<int>(n), W, run, order, tiles, static_cast<int>(hq_lora_max_tiles(M, n)));
-    return cudaGetLastError() == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cl);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cl;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cl > 1 ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_lora_plan, ids, static_cast<int>(M), static_cast<int>(n), W, run, order,
+                                             tiles, static_cast<int>(hq_lora_max_tiles(M, n)));
+    return e == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
 }
 
 extern "C" size_t hq_lora_workspace_size(int64_t M, int32_t r_max) {
