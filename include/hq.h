@@ -545,7 +545,7 @@ hq_status hq_mxfp4_linear(const uint8_t* Xq, const uint8_t* sx, int64_t M, int64
  * A row's outputs depend on that row alone (NaN and infinities stay in it).
  * Errors: HQ_ERR_ARG (M < 0, K <= 0, a bad type, a stride below K, eps negative or
  * NaN, gate or w_post without Y, w without X or X without w, no output, H NULL with
- * M > 0), HQ_ERR_ALIGN, HQ_ERR_UNSUPPORTED (K > 16384, M above INT32_MAX),
+ * M > 0, H_out equal to X, an output equal to H or Y with another stride), HQ_ERR_ALIGN, HQ_ERR_UNSUPPORTED (K > 16384, M above INT32_MAX),
  * HQ_ERR_CUDA.  M == 0 is a no-op.
  */
 hq_status hq_residual_norm(const void* H, int64_t ld_h, const void* Y, int64_t ld_y, hq_dtype xt, int64_t M, int64_t K,

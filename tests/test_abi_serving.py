@@ -21,8 +21,11 @@ def lib():
     return _lib.lib
 
 
-def norm(lib, H=P, ldh=256, Y=P, ldy=256, xt=F16, M=4, K=256, wp=None, gate=None, ldg=0, alpha=1.0, w=P, wt=F16,
-         off=0.0, eps=1e-5, Ho=P, ldho=256, X=P, ldx=256):
+P2, P3 = ct.c_void_p(32), ct.c_void_p(48)
+
+
+def norm(lib, H=P, ldh=256, Y=P2, ldy=256, xt=F16, M=4, K=256, wp=None, gate=None, ldg=0, alpha=1.0, w=P, wt=F16,
+         off=0.0, eps=1e-5, Ho=P, ldho=256, X=P2, ldx=256):
     return lib.hq_residual_norm(H, ldh, Y, ldy, xt, M, K, wp, gate, ldg, alpha, w, wt, off, eps, Ho, ldho, X, ldx, None)
 
 
@@ -32,10 +35,12 @@ def norm(lib, H=P, ldh=256, Y=P, ldy=256, xt=F16, M=4, K=256, wp=None, gate=None
     (dict(ldh=255), ARG), (dict(ldy=248), ARG), (dict(ldho=8), ARG), (dict(ldx=0), ARG),
     (dict(gate=P, ldg=128), ARG),
     (dict(Y=None, gate=P), ARG), (dict(Y=None, wp=P), ARG),
+    (dict(Ho=P3, X=P3), ARG), (dict(ldho=264), ARG), (dict(ldx=264), ARG), (dict(Ho=P2, X=P3, ldho=264), ARG),
+    (dict(X=P, Ho=P3, ldx=264), ARG),
     (dict(w=None), ARG), (dict(X=None), ARG), (dict(w=None, X=None, Ho=None), ARG), (dict(H=None), ARG),
     (dict(H=ODD), ALIGN), (dict(Y=ODD), ALIGN), (dict(gate=ODD), ALIGN), (dict(wp=ODD), ALIGN), (dict(w=ODD), ALIGN),
     (dict(Ho=ODD), ALIGN), (dict(X=ODD), ALIGN),
-    (dict(ldh=260), ALIGN), (dict(ldx=260), ALIGN), (dict(xt=F32, ldy=258), ALIGN), (dict(gate=P, ldg=260), ALIGN),
+    (dict(Ho=P3, ldh=260), ALIGN), (dict(X=P3, ldx=260), ALIGN), (dict(xt=F32, X=P3, ldy=258), ALIGN), (dict(gate=P, ldg=260), ALIGN),
     (dict(K=16385, ldh=16392, ldy=16392, ldho=16392, ldx=16392), UNSUPPORTED), (dict(M=1 << 31), UNSUPPORTED),
     (dict(M=0, H=None, Y=None, w=None, X=None, Ho=None), OK), (dict(M=0), OK),
 ])
@@ -43,7 +48,7 @@ def test_residual_norm_refusals(lib, kw, want):
     assert norm(lib, **kw) == want
 
 
-def normq(lib, H=P, ldh=256, Y=P, ldy=256, xt=F16, M=4, K=256, gate=None, ldg=0, w=P, wt=F16, eps=1e-5, group=128,
+def normq(lib, H=P, ldh=256, Y=P2, ldy=256, xt=F16, M=4, K=256, gate=None, ldg=0, w=P, wt=F16, eps=1e-5, group=128,
           d=None, bits=4, Ho=P, ldho=256, X=None, ldx=0, Xq=P, sx=P):
     return lib.hq_norm_rotate_quant(H, ldh, Y, ldy, xt, M, K, gate, ldg, 1.0, w, wt, 0.0, eps, group, d, bits, Ho, ldho,
                                     X, ldx, Xq, sx, None)
@@ -55,7 +60,7 @@ def normq(lib, H=P, ldh=256, Y=P, ldy=256, xt=F16, M=4, K=256, gate=None, ldg=0,
     (dict(bits=5), ARG), (dict(bits=16), ARG), (dict(M=-1), ARG), (dict(wt=3), ARG), (dict(xt=9), ARG),
     (dict(xt=F32), UNSUPPORTED), (dict(K=32768, ldh=32768, ldy=32768, ldho=32768), UNSUPPORTED),
     (dict(w=None), ARG), (dict(Xq=None), ARG), (dict(sx=None), ARG), (dict(H=None), ARG), (dict(Y=None, gate=P), ARG),
-    (dict(Xq=ODD), ALIGN), (dict(X=ODD, ldx=256), ALIGN), (dict(X=P, ldx=128), ARG), (dict(ldh=260), ALIGN),
+    (dict(Xq=ODD), ALIGN), (dict(X=ODD, ldx=256), ALIGN), (dict(X=P3, ldx=128), ARG), (dict(Ho=P3, ldh=260), ALIGN),
     (dict(M=0, H=None, w=None, Xq=None, sx=None), OK),
 ])
 def test_norm_rotate_quant_refusals(lib, kw, want):

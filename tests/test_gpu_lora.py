@@ -155,6 +155,16 @@ def apply(d, plan=None, **kw):
     (500, 136, 88, 30, 128, F16, F16, True, 1),
     (1000, 4096, 1024, 3, 256, BF16, F32, True, 100),
     (2048, 11008, 512, 8, 32, BF16, BF16, False, 256),
+    # whole tiles: odd and even numbers of them per adapter, last ones not full, every rank class
+    (700, 256, 8, 2, 8, BF16, BF16, False, 100),
+    (1111, 128, 72, 3, 24, F16, F16, True, 193),
+    (900, 64, 200, 2, 56, BF16, F32, True, 320),
+    (1500, 384, 136, 4, 96, F16, BF16, True, 130),
+    (640, 200, 640, 1, 128, BF16, F16, True, 640),
+    (700, 128, 320, 2, 192, BF16, F32, True, 70),
+    (800, 128, 192, 1, 200, F16, F32, True, 800),
+    (513, 128, 264, 2, 256, BF16, BF16, True, 171),
+    (513, 128, 264, 2, 256, F16, F32, True, 171),
 ])
 def test_apply(M, K, N, n, r, xt, yt, ragged, runs):
     d = batch(M, K, N, n, r, xt, yt, seed=M + K, ragged=ragged, runs=runs)
@@ -167,9 +177,10 @@ def test_apply(M, K, N, n, r, xt, yt, ragged, runs):
     assert torch.equal(apply(d, Y=d["base"]), Y) and torch.equal(d["base"], Y)   # in place
 
 
+@pytest.mark.parametrize("M,runs", [(130, 13), (5, 1)])
 @pytest.mark.parametrize("yt", [F16, BF16, F32])
-def test_no_base_no_ranks_no_scales(yt):
-    d = batch(130, 256, 136, 3, 16, BF16, yt, ragged=False, runs=13)
+def test_no_base_no_ranks_no_scales(yt, M, runs):
+    d = batch(M, 256, 136, 3, 16, BF16, yt, ragged=False, runs=runs)
     d["scales"] = None
     Y = apply(d, base=None, out_dtype=yt)
     check(Y, d, base=False)
@@ -202,16 +213,17 @@ def test_strided_rows_and_nothing_else_written():
     assert (ybuf[77:] == 9).all() and (ybuf[:, 136:] == 9).all() and (work[77 * 24:] == 5).all()
 
 
-def test_values_of_one_token_stay_with_it():
-    d = batch(50, 192, 64, 3, 16, BF16, BF16, runs=5)
+@pytest.mark.parametrize("M,xt", [(50, BF16), (50, F16), (400, BF16), (400, F16)])
+def test_values_of_one_token_stay_with_it(M, xt):
+    d = batch(M, 192, 64, 3, 16, xt, BF16, runs=M // 10)
     want = apply(d)
     ids = d["ids"].tolist()
-    odd = [m for m in range(50) if ids[m] >= 0][:2] + [m for m in range(50) if ids[m] < 0][:1]
+    odd = [m for m in range(M) if ids[m] >= 0][:2] + [m for m in range(M) if ids[m] < 0][:1]
     d["X"][odd[0], 7] = float("nan")
     d["X"][odd[1], 100] = float("inf")
     d["X"][odd[2]] = float("nan")             # a token without an adapter: its input is not used
     got = apply(d)
-    for m in range(50):
+    for m in range(M):
         if m not in odd[:2]:
             assert torch.equal(got[m], want[m])
     if d["ranks"][ids[odd[0]]] > 0:
@@ -348,3 +360,40 @@ def test_layer_with_adapters(kind, M):
     assert torch.equal(Y2, apply({**d, "X": x2, "base": base2}, plan))
     layer.set_adapters(None, None)
     assert torch.equal(layer(d["X"]), d["base"])
+
+
+def test_a_decoder_step_captured():
+    """Plan, norm + quantiser + layer + adapters, and the next layer's norm on the
+    updated stream, as one captured step: replays with other tokens and other
+    adapters give what the calls give one by one."""
+    M, K, n, r = 24, 1024, 4, 16
+    d = batch(M, K, K, n, r, BF16, BF16, seed=3)
+    up = hq.W4A4Linear.prepare(randn((K, K), F32, 20, 0.03), 128, 128, 16, X_calib=randn((64, K), BF16, 21))
+    down = hq.W4A4Linear.prepare(randn((K, K), F32, 22, 0.03), 128, 128, 16, X_calib=randn((64, K), BF16, 23), act_bits=8)
+    up.set_adapters(d["A"], d["B"], d["ranks"], d["scales"])
+    down.set_adapters(d["A"], d["B"], d["ranks"], d["scales"])
+    w1, w2, w3 = (1 + randn((K,), BF16, 24 + k, 0.2) for k in range(3))
+
+    def step(H, block, ids):
+        plan = hq.hq_lora_plan(ids, n)
+        y, h = up.forward_normed(H, w1, 1e-5, block=block, plan=plan)
+        z, h = down.forward_normed(h, w2, 1e-5, block=y, alpha=0.5, plan=plan)
+        return hq.hq_residual_norm(h, w3, 1e-5, Y=z, w_post=w1)
+
+    H, block, ids = torch.zeros(M, K, dtype=BF16, device="cuda"), torch.zeros(M, K, dtype=BF16, device="cuda"), d["ids"].clone()
+    step(H, block, ids)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(H, block, ids)
+    for seed in range(3):
+        H.copy_(randn((M, K), BF16, 30 + seed, 2.0))
+        block.copy_(randn((M, K), BF16, 40 + seed))
+        ids.copy_(torch.randint(-1, n, (M,), generator=torch.Generator().manual_seed(seed)).to(torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        want = step(H, block, ids)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert got[1].isfinite().all()
+    assert hq.hq_last_device_status() == 0

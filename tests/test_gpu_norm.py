@@ -88,6 +88,12 @@ CASES = [
     (3, 8192, BF16, F32, False, "channel", 0.5, 0.0, 0),
     (2, 16383, F16, F32, True, "token", 1.0, 0.0, 0),
     (2, 16384, F32, F32, True, "token", 1.0, 0.0, 0),
+    # several rows per CTA
+    (9001, 100, BF16, F32, True, "token", 1.0, 0.0, 0),
+    (6000, 512, F16, BF16, False, "channel", 0.5, 1.0, 8),
+    (2500, 6144, BF16, F16, True, "token", 1.0, 0.0, 0),
+    (2000, 10000, F16, F32, True, "channel", 1.0, 0.0, 0),
+    (3000, 1301, F32, F16, False, None, 1.0, 0.0, 4),
 ]
 
 
@@ -232,6 +238,11 @@ QCASES = [
     (5, 6144, 2048, 4, F16, F32, True, "token", 1.0, 0.0, True),
     (6, 4096, 4096, 8, BF16, BF16, True, None, 1.0, 0.0, True),
     (2, 16384, 4096, 4, F16, F16, True, None, 1.0, 0.0, True),
+    # several rows per CTA
+    (9001, 96, 32, 4, F16, F16, True, "token", 1.0, 0.0, True),
+    (5000, 1024, 8, 8, BF16, F32, False, None, 1.0, 0.0, True),
+    (3001, 1536, 512, 4, BF16, BF16, True, "channel", 0.5, 0.0, True),
+    (1501, 4096, 2048, 8, F16, F32, True, None, 1.0, 0.0, True),
 ]
 
 

@@ -199,44 +199,38 @@ __device__ __forceinline__ float4 add4(float4 a, float4 b) {
     return make_float4(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y), __fadd_rn(a.z, b.z), __fadd_rn(a.w, b.w));
 }
 
-// One tile and RC columns of the rank per cluster; CTA q of the cluster sums
-// its run of K.  Stages of 128 channels stream through a cp.async ring as two
-// halves of 128-byte rows (16-byte chunk c of row i at chunk c ^ (i & 7)).
-// Warp (h, w) takes 32 of the tile's tokens and channels 16 w .. 16 w + 15 of
-// each half.  The partial sums meet in a fixed order: over the CTA's warps,
-// then over the cluster.
-template <bool BF, int RC>
-__global__ void __launch_bounds__(SH_THREADS) k_lora_shrink(const ShrinkArgs p) {
-    constexpr int HALF = (LR_TILE + RC) * 128, STAGE = 2 * HALF;
-    extern __shared__ __align__(128) uint8_t sm[];
-    asm volatile("griddepcontrol.launch_dependents;");
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int q = blockIdx.x, cl = gridDim.x;   // rank in the cluster, its CTAs
-    const int a = p.tiles[3 * blockIdx.y], start = p.tiles[3 * blockIdx.y + 1], count = p.tiles[3 * blockIdx.y + 2];
-    if (a < 0 || count == 0) return;   // no adapter, or an unused tile: the whole cluster leaves
+// Tile i and the rank of its adapter; false where there is nothing to do (no
+// adapter, an unused or a bad entry)
+__device__ __forceinline__ bool shrink_tile(const ShrinkArgs& p, int i, int& a, int& start, int& count, int& live) {
+    a = p.tiles[3 * i];
+    start = p.tiles[3 * i + 1];
+    count = p.tiles[3 * i + 2];
+    if (a < 0 || count == 0) return false;
     if (a >= p.n || count < 0 || count > LR_TILE || start < 0 || start > p.M - count) {
-        if (tid == 0) record_status(HQ_ERR_ARG);
-        return;
+        if (threadIdx.x == 0) record_status(HQ_ERR_ARG);
+        return false;
     }
-    const int r0 = blockIdx.z * RC;
-    int live = p.r;
+    live = p.r;
     if (p.ranks != nullptr) {
         live = p.ranks[a];
         if (live < 0 || live > p.r) {
-            if (tid == 0) record_status(HQ_ERR_ARG);
+            if (threadIdx.x == 0) record_status(HQ_ERR_ARG);
             live = live < 0 ? 0 : p.r;
         }
     }
-    live = min(max(live - r0, 0), RC);
-    if (live == 0) {   // the adapter's rank ends before these columns
-        for (int i = q * SH_THREADS + tid; i < count * (RC / 4); i += cl * SH_THREADS) {
-            const int row = i / (RC / 4), col = r0 + i % (RC / 4) * 4;
-            if (col < p.r)
-                *reinterpret_cast<float4*>(p.T + static_cast<int64_t>(start + row) * p.r + col) = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        return;
-    }
+    return true;
+}
 
+// The sums of one tile and RC columns of the rank over CTA q's part of K (of cl
+// parts), left in `sm` as [token][RC].  Stages of 128 channels stream through a
+// cp.async ring as two halves of 128-byte rows (16-byte chunk c of row i at
+// chunk c ^ (i & 7)).  Warp (h, w) takes 32 of the tile's tokens and channels
+// 16 w .. 16 w + 15 of each half; the warps' sums meet in a fixed order.
+template <bool BF, int RC>
+__device__ __forceinline__ void shrink_part(const ShrinkArgs& p, int a, int start, int count, int r0, int live, int q,
+                                            int cl, uint8_t* sm) {
+    constexpr int HALF = (LR_TILE + RC) * 128, STAGE = 2 * HALF;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // this thread's rows of a stage: tokens tid/16 + 16 j, adapter rows the same
     const int crow = tid >> 4, chunk = tid & 15;
     const uint16_t* xsrc[LR_TILE / 16];
@@ -341,6 +335,31 @@ __global__ void __launch_bounds__(SH_THREADS) k_lora_shrink(const ShrinkArgs p) 
         for (int w = 1; w < 4; ++w) v = add4(v, part4[w * LR_TILE * (RC / 4) + i]);
         part4[i] = v;
     }
+}
+
+// One tile and RC columns of the rank per cluster, CTA q a part of K; the partial
+// sums meet in a fixed order over the cluster.
+template <bool BF, int RC>
+__global__ void __launch_bounds__(SH_THREADS) k_lora_shrink(const ShrinkArgs p) {
+    extern __shared__ __align__(128) uint8_t sm[];
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int tid = threadIdx.x;
+    const int q = blockIdx.x, cl = gridDim.x;   // rank in the cluster, its CTAs
+    int a, start, count, live;
+    if (!shrink_tile(p, blockIdx.y, a, start, count, live)) return;   // the whole cluster leaves
+    const int r0 = blockIdx.z * RC;
+    live = min(max(live - r0, 0), RC);
+    if (live == 0) {   // the adapter's rank ends before these columns
+        for (int i = q * SH_THREADS + tid; i < count * (RC / 4); i += cl * SH_THREADS) {
+            const int row = i / (RC / 4), col = r0 + i % (RC / 4) * 4;
+            if (col < p.r)
+                *reinterpret_cast<float4*>(p.T + static_cast<int64_t>(start + row) * p.r + col) = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        return;
+    }
+
+    shrink_part<BF, RC>(p, a, start, count, r0, live, q, cl, sm);
+    const float4* part4 = reinterpret_cast<const float4*>(sm);
     cluster_sync();
     const float scale = p.scales != nullptr ? p.scales[a] : 1.f;
     for (int i = q * SH_THREADS + tid; i < count * (RC / 4); i += cl * SH_THREADS) {
@@ -363,6 +382,8 @@ __global__ void __launch_bounds__(SH_THREADS) k_lora_shrink(const ShrinkArgs p) 
 }
 
 // ---------------------------------------------------------------------- expand
+constexpr uint64_t EX_LIMIT_NS = 2000000000ull;   // of a wait
+
 struct ExpandArgs {
     const float* T;
     const uint16_t* B;
@@ -409,7 +430,18 @@ __device__ __forceinline__ uint32_t narrow16(bool bf, float a, float b) {
 
 // The tile's rows of Y are its rows of base (or zero): tokens without an adapter
 template <int YT>
-__device__ void copy_rows(const ExpandArgs& p, const Tile& t, int col0, int cols) {
+__device__ void copy_cols(const ExpandArgs& p, const Tile& t, int col0, int cols);
+
+// part q of cl of all columns
+template <int YT>
+__device__ void copy_rows(const ExpandArgs& p, const Tile& t, int q, int cl) {
+    const int eights = p.N / 8;
+    const int a = static_cast<int>(static_cast<int64_t>(q) * eights / cl), b = static_cast<int>(static_cast<int64_t>(q + 1) * eights / cl);
+    copy_cols<YT>(p, t, 8 * a, 8 * (b - a));
+}
+
+template <int YT>
+__device__ void copy_cols(const ExpandArgs& p, const Tile& t, int col0, int cols) {
     if (p.base == p.Y) return;   // in place
     constexpr int PER = 16 / out_bytes<YT>;
     const int vecs = (min(cols, p.N - col0)) / PER;   // N is a multiple of 8
@@ -471,7 +503,7 @@ __global__ void __launch_bounds__(FEW_THREADS) k_lora_expand_few(const ExpandArg
     }
     griddep_wait();   // t is complete
     if (t.live == 0) {
-        copy_rows<YT>(p, t, blockIdx.x * FEW_COLS, FEW_COLS);
+        copy_cols<YT>(p, t, blockIdx.x * FEW_COLS, FEW_COLS);
         return;
     }
     for (int i0 = 0; i0 < t.count; i0 += 4) {
@@ -517,6 +549,123 @@ __global__ void __launch_bounds__(FEW_THREADS) k_lora_expand_few(const ExpandArg
     }
 }
 
+// Few tokens per tile, both products in one launch: a cluster of 8 CTAs forms a
+// tile's t (each a part of K), every CTA reads the partial sums of all of them
+// from their shared memory, and then each takes an eighth of the columns, as in
+// k_lora_expand_few, two neighbouring ones a thread, with the next pair's B and
+// base loaded a round ahead.  Ranks up to 64; t has no place in memory.  Against
+// the two kernels it takes 1 us longer on the GPU but 2.5 us less of the host,
+// which is what a single step waits for.  (Staging all of the CTA's B by bulk
+// copies of one pair of rows each took 3 us more: they are too small.)
+template <int RC>
+constexpr int few_ring = SH_STAGES * (LR_TILE + RC) * 256 > 4 * LR_TILE * RC * 4 ? SH_STAGES * (LR_TILE + RC) * 256
+                                                                                 : 4 * LR_TILE * RC * 4;
+
+template <bool BF, int YT, int RC>
+__global__ void __launch_bounds__(SH_THREADS) k_lora_few(const ShrinkArgs sp, const ExpandArgs p) {
+    extern __shared__ __align__(128) uint8_t sm[];   // the ring, later the partial sums; t [64][RC]
+    __shared__ int rows[LR_TILE];
+    float* tt = reinterpret_cast<float*>(sm + few_ring<RC>);
+    const int tid = threadIdx.x, q = blockIdx.x, cl = gridDim.x;
+    // this CTA's columns, in pairs
+    const int eights = p.N / 8, c0 = 4 * static_cast<int>(static_cast<int64_t>(q) * eights / cl),
+              c1 = 4 * static_cast<int>(static_cast<int64_t>(q + 1) * eights / cl);
+    const Tile t = tile_of(p, blockIdx.y);
+    {
+        int a, start, count, live;
+        shrink_tile(sp, blockIdx.y, a, start, count, live);   // reports a bad entry or rank
+    }
+    if (t.live == 0) {
+        copy_rows<YT>(p, t, q, cl);
+        return;   // the whole cluster leaves
+    }
+    if (tid < LR_TILE) {
+        const int m = tid < t.count ? p.order[t.start + tid] : -1;
+        rows[tid] = m < p.M ? m : -1;
+    }
+    const uint16_t* bcol = p.B + static_cast<int64_t>(t.a) * p.N * p.r;
+    uint4 b[2][RC / 8];   // column, eight rank positions
+    auto load_b = [&](int c) {
+        const uint16_t* s = bcol + static_cast<int64_t>(2 * c) * p.r;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < RC / 8; ++e)
+                b[k][e] = c < c1 && 8 * e < t.live ? __ldg(reinterpret_cast<const uint4*>(s + k * p.r) + e)
+                                                   : make_uint4(0u, 0u, 0u, 0u);
+    };
+    if constexpr (RC <= 32) load_b(c0 + tid);   // before t is formed
+    shrink_part<BF, RC>(sp, t.a, t.start, t.count, 0, t.live, q, cl, sm);
+    cluster_sync();
+    {
+        const float scale = sp.scales != nullptr ? sp.scales[t.a] : 1.f;
+        const float4* part4 = reinterpret_cast<const float4*>(sm);
+        for (int i = tid; i < t.count * (RC / 4); i += SH_THREADS) {
+            float4 u[SH_MAX_CL];
+#pragma unroll
+            for (int c = 0; c < SH_MAX_CL; ++c)
+                if (c < cl) u[c] = ld_cluster_f32x4(mapa_shared(smem_u32(part4 + i), c));
+            float4 v = u[0];
+#pragma unroll
+            for (int c = 1; c < SH_MAX_CL; ++c)
+                if (c < cl) v = add4(v, u[c]);
+            const int col = i % (RC / 4) * 4;
+            v.x = col < t.live ? __fmul_rn(v.x, scale) : 0.f;
+            v.y = col + 1 < t.live ? __fmul_rn(v.y, scale) : 0.f;
+            v.z = col + 2 < t.live ? __fmul_rn(v.z, scale) : 0.f;
+            v.w = col + 3 < t.live ? __fmul_rn(v.w, scale) : 0.f;
+            reinterpret_cast<float4*>(tt)[i] = v;
+        }
+    }
+    // base of the first token and pair, then a pair ahead
+    auto base_at = [&](int m, int c) {
+        if (p.base == nullptr || m < 0 || c >= c1) return make_float2(0.f, 0.f);
+        const uint8_t* s = static_cast<const uint8_t*>(p.base) + (m * p.ldb + 2 * c) * out_bytes<YT>;
+        return YT == HQ_F32 ? *reinterpret_cast<const float2*>(s) : widen16(YT == HQ_BF16, *reinterpret_cast<const uint32_t*>(s));
+    };
+    float2 ynext = base_at(rows[0], c0 + tid);
+    cluster_sync();   // t is there, and nobody reads another CTA's sums any more
+    if constexpr (RC > 32) load_b(c0 + tid);
+    for (int c = c0 + tid; c < c1; c += SH_THREADS) {
+        float w[2][RC];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < RC / 8; ++e) {
+                const uint32_t x[4] = {b[k][e].x, b[k][e].y, b[k][e].z, b[k][e].w};
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float2 f = widen16(BF, x[u]);
+                    // past the adapter's rank B is not read as a number
+                    w[k][8 * e + 2 * u] = 8 * e + 2 * u < t.live ? f.x : 0.f;
+                    w[k][8 * e + 2 * u + 1] = 8 * e + 2 * u + 1 < t.live ? f.y : 0.f;
+                }
+            }
+        load_b(c + SH_THREADS);
+        for (int i = 0; i < t.count; ++i) {
+            const int m = rows[i];
+            const float2 y = ynext;
+            ynext = i + 1 < t.count ? base_at(rows[i + 1], c) : base_at(rows[0], c + SH_THREADS);
+            if (m < 0) continue;
+            float acc[2] = {0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < RC; j += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(tt + i * RC + j);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    acc[k] = __fmaf_rn(v.w, w[k][j + 3],
+                                       __fmaf_rn(v.z, w[k][j + 2], __fmaf_rn(v.y, w[k][j + 1], __fmaf_rn(v.x, w[k][j], acc[k]))));
+            }
+            uint8_t* d = static_cast<uint8_t*>(p.Y) + (m * p.ldy + 2 * c) * out_bytes<YT>;
+            const float v0 = __fadd_rn(y.x, acc[0]), v1 = __fadd_rn(y.y, acc[1]);
+            if constexpr (YT == HQ_F32)
+                *reinterpret_cast<float2*>(d) = make_float2(v0, v1);
+            else
+                *reinterpret_cast<uint32_t*>(d) = narrow16(YT == HQ_BF16, v0, v1);
+        }
+    }
+}
+
 // Whole tiles (prompts): t of two tiles (128 tokens) and blocks of 64 rows of B
 // are operands of tcgen05.mma (kind::f16, 128 x 64, fp32 accumulators in tensor
 // memory), so that the warps are left with what HBM sees: base in, Y out.
@@ -537,7 +686,6 @@ __global__ void __launch_bounds__(FEW_THREADS) k_lora_expand_few(const ExpandArg
 constexpr int EX_THREADS = 256;                 // those that copy and store
 constexpr int EX_ROWS = 2 * LR_TILE;            // tokens of a product
 constexpr int EX_NB = 64;                       // columns of a block
-constexpr uint64_t EX_LIMIT_NS = 2000000000ull;
 
 __host__ __device__ constexpr int ex_terms(bool bf, int yt) { return bf && yt == HQ_F32 ? 3 : 2; }
 // bytes of shared memory: t, two blocks of B, base (`depth` blocks), row scales
@@ -596,7 +744,7 @@ __global__ void __launch_bounds__(EX_THREADS + 32, 2) k_lora_expand(const Expand
     const Tile t = tile_of(p, ti);
     if (t.live == 0) {   // the same for the whole CTA
         griddep_wait();
-        copy_rows<YT>(p, t, blk0 * EX_NB, (blk1 - blk0) * EX_NB);
+        copy_cols<YT>(p, t, blk0 * EX_NB, (blk1 - blk0) * EX_NB);
         return;
     }
     int before = 0;
@@ -960,15 +1108,44 @@ hq_status launch_expand(ExpandArgs a, int tiles, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
 }
 
-template <bool BF>
-hq_status launch_lora(const ShrinkArgs& s, const ExpandArgs& e, int yt, int tiles, cudaStream_t st) {
+template <bool BF, int YT, int RC>
+hq_status launch_few(const ShrinkArgs& s, const ExpandArgs& e, int tiles, cudaStream_t st) {
+    constexpr int smem = few_ring<RC> + LR_TILE * RC * 4;
+    auto kern = k_lora_few<BF, YT, RC>;
+    static SmemOptIn opt_in;
+    if (!allow_smem(opt_in, kern, smem)) return HQ_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(SH_MAX_CL, tiles);
+    cfg.blockDim = dim3(SH_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = SH_MAX_CL;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, s, e) == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
+}
+
+template <bool BF, int YT>
+hq_status launch_lora_y(const ShrinkArgs& s, const ExpandArgs& e, int tiles, cudaStream_t st) {
+    if (s.M < 16 * tiles && s.r <= 64)
+        return s.r <= 16   ? launch_few<BF, YT, 16>(s, e, tiles, st)
+               : s.r <= 32 ? launch_few<BF, YT, 32>(s, e, tiles, st)
+                           : launch_few<BF, YT, 64>(s, e, tiles, st);
     const hq_status r = s.r <= 16 ? launch_shrink<BF, 16>(s, tiles, st)
                         : s.r <= 32 ? launch_shrink<BF, 32>(s, tiles, st)
                                     : launch_shrink<BF, 64>(s, tiles, st);
-    if (r != HQ_OK) return r;
-    if (yt == HQ_F16) return launch_expand<BF, HQ_F16>(e, tiles, st);
-    if (yt == HQ_BF16) return launch_expand<BF, HQ_BF16>(e, tiles, st);
-    return launch_expand<BF, HQ_F32>(e, tiles, st);
+    return r != HQ_OK ? r : launch_expand<BF, YT>(e, tiles, st);
+}
+
+template <bool BF>
+hq_status launch_lora(const ShrinkArgs& s, const ExpandArgs& e, int yt, int tiles, cudaStream_t st) {
+    if (yt == HQ_F16) return launch_lora_y<BF, HQ_F16>(s, e, tiles, st);
+    if (yt == HQ_BF16) return launch_lora_y<BF, HQ_BF16>(s, e, tiles, st);
+    return launch_lora_y<BF, HQ_F32>(s, e, tiles, st);
 }
 
 }  // namespace

@@ -680,6 +680,11 @@ hq_status nm_check(const NormArgs& a, int64_t M, int64_t K, int xt) {
     if (a.ldh < K || (a.Y && a.ldy < K) || (a.Ho && a.ldho < K) || (a.X && a.ldx < K)) return HQ_ERR_ARG;
     if (a.gate && a.ldg != 0 && a.ldg < K) return HQ_ERR_ARG;
     if (!a.Y && (a.gate || a.w_post)) return HQ_ERR_ARG;
+    // in place means the same place: rows of another stride would overlap
+    if (a.Ho && a.Ho == a.X) return HQ_ERR_ARG;
+    if ((a.Ho == a.H && a.Ho && a.ldho != a.ldh) || (a.Ho == a.Y && a.Y && a.ldho != a.ldy) ||
+        (a.X == a.H && a.X && a.ldx != a.ldh) || (a.X == a.Y && a.Y && a.ldx != a.ldy))
+        return HQ_ERR_ARG;
     if (M > INT32_MAX || K > NM_MAXK) return HQ_ERR_UNSUPPORTED;
     if (!a.H) return HQ_ERR_ARG;
     const int64_t es = xt == HQ_F32 ? 4 : 2;
