@@ -199,25 +199,40 @@ __device__ __forceinline__ float4 add4(float4 a, float4 b) {
     return make_float4(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y), __fadd_rn(a.z, b.z), __fadd_rn(a.w, b.w));
 }
 
-// Tile i and the rank of its adapter; false where there is nothing to do (no
-// adapter, an unused or a bad entry)
-__device__ __forceinline__ bool shrink_tile(const ShrinkArgs& p, int i, int& a, int& start, int& count, int& live) {
-    a = p.tiles[3 * i];
-    start = p.tiles[3 * i + 1];
-    count = p.tiles[3 * i + 2];
-    if (a < 0 || count == 0) return false;
-    if (a >= p.n || count < 0 || count > LR_TILE || start < 0 || start > p.M - count) {
+// What a thread needs of tile i: the tile, its adapter's rank, and the tokens
+// whose rows the thread copies (tid / 16 + 16 j of the tile, -1 for none).  Two
+// dependent loads in all: the rank and the tokens are asked for together.  False
+// where there is nothing to do (no adapter, an unused or a bad entry).
+struct ShrinkTile {
+    int a, start, count, live;
+    int m[LR_TILE / 16];
+};
+
+__device__ __forceinline__ bool shrink_tile(const ShrinkArgs& p, int i, ShrinkTile& t) {
+    t.a = p.tiles[3 * i];
+    t.start = p.tiles[3 * i + 1];
+    t.count = p.tiles[3 * i + 2];
+    if (t.a < 0 || t.count == 0) return false;
+    if (t.a >= p.n || t.count < 0 || t.count > LR_TILE || t.start < 0 || t.start > p.M - t.count) {
         if (threadIdx.x == 0) record_status(HQ_ERR_ARG);
         return false;
     }
-    live = p.r;
-    if (p.ranks != nullptr) {
-        live = p.ranks[a];
-        if (live < 0 || live > p.r) {
-            if (threadIdx.x == 0) record_status(HQ_ERR_ARG);
-            live = live < 0 ? 0 : p.r;
+    const int row = threadIdx.x >> 4;
+#pragma unroll
+    for (int j = 0; j < LR_TILE / 16; ++j) t.m[j] = row + 16 * j < t.count ? p.order[t.start + row + 16 * j] : 0;
+    t.live = p.ranks != nullptr ? p.ranks[t.a] : p.r;
+    bool bad = t.live < 0 || t.live > p.r;
+    t.live = min(max(t.live, 0), p.r);
+#pragma unroll
+    for (int j = 0; j < LR_TILE / 16; ++j)
+        if (t.m[j] < 0 || t.m[j] >= p.M) {
+            bad = true;
+            t.m[j] = -1;
         }
-    }
+    if (bad) record_status(HQ_ERR_ARG);
+#pragma unroll
+    for (int j = 0; j < LR_TILE / 16; ++j)
+        if (row + 16 * j >= t.count) t.m[j] = -1;
     return true;
 }
 
@@ -227,26 +242,16 @@ __device__ __forceinline__ bool shrink_tile(const ShrinkArgs& p, int i, int& a, 
 // chunk c ^ (i & 7)).  Warp (h, w) takes 32 of the tile's tokens and channels
 // 16 w .. 16 w + 15 of each half; the warps' sums meet in a fixed order.
 template <bool BF, int RC>
-__device__ __forceinline__ void shrink_part(const ShrinkArgs& p, int a, int start, int count, int r0, int live, int q,
-                                            int cl, uint8_t* sm) {
+__device__ __forceinline__ void shrink_part(const ShrinkArgs& p, const ShrinkTile& t, int r0, int live, int q, int cl,
+                                            uint8_t* sm) {
     constexpr int HALF = (LR_TILE + RC) * 128, STAGE = 2 * HALF;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // this thread's rows of a stage: tokens tid/16 + 16 j, adapter rows the same
-    const int crow = tid >> 4, chunk = tid & 15;
+    const int count = t.count, crow = tid >> 4, chunk = tid & 15;
     const uint16_t* xsrc[LR_TILE / 16];
 #pragma unroll
-    for (int j = 0; j < LR_TILE / 16; ++j) {
-        const int i = crow + 16 * j;
-        xsrc[j] = nullptr;
-        if (i < count) {
-            const int m = p.order[start + i];
-            if (m >= 0 && m < p.M)
-                xsrc[j] = p.X + m * p.ldx + chunk * 8;
-            else
-                record_status(HQ_ERR_ARG);
-        }
-    }
-    const uint16_t* asrc = p.A + (static_cast<int64_t>(a) * p.r + r0 + crow) * p.K + chunk * 8;
+    for (int j = 0; j < LR_TILE / 16; ++j) xsrc[j] = t.m[j] >= 0 ? p.X + t.m[j] * p.ldx + chunk * 8 : nullptr;
+    const uint16_t* asrc = p.A + (static_cast<int64_t>(t.a) * p.r + r0 + crow) * p.K + chunk * 8;
     const uint32_t ring = smem_u32(sm);
     const uint32_t dst = (chunk >> 3) * HALF + crow * 128 + (((chunk & 7) ^ (crow & 7)) << 4);
 
@@ -345,10 +350,10 @@ __global__ void __launch_bounds__(SH_THREADS) k_lora_shrink(const ShrinkArgs p) 
     asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x;
     const int q = blockIdx.x, cl = gridDim.x;   // rank in the cluster, its CTAs
-    int a, start, count, live;
-    if (!shrink_tile(p, blockIdx.y, a, start, count, live)) return;   // the whole cluster leaves
-    const int r0 = blockIdx.z * RC;
-    live = min(max(live - r0, 0), RC);
+    ShrinkTile t;
+    if (!shrink_tile(p, blockIdx.y, t)) return;   // the whole cluster leaves
+    const int start = t.start, count = t.count;
+    const int r0 = blockIdx.z * RC, live = min(max(t.live - r0, 0), RC);
     if (live == 0) {   // the adapter's rank ends before these columns
         for (int i = q * SH_THREADS + tid; i < count * (RC / 4); i += cl * SH_THREADS) {
             const int row = i / (RC / 4), col = r0 + i % (RC / 4) * 4;
@@ -358,10 +363,10 @@ __global__ void __launch_bounds__(SH_THREADS) k_lora_shrink(const ShrinkArgs p) 
         return;
     }
 
-    shrink_part<BF, RC>(p, a, start, count, r0, live, q, cl, sm);
+    shrink_part<BF, RC>(p, t, r0, live, q, cl, sm);
     const float4* part4 = reinterpret_cast<const float4*>(sm);
     cluster_sync();
-    const float scale = p.scales != nullptr ? p.scales[a] : 1.f;
+    const float scale = p.scales != nullptr ? p.scales[t.a] : 1.f;
     for (int i = q * SH_THREADS + tid; i < count * (RC / 4); i += cl * SH_THREADS) {
         float4 u[SH_MAX_CL];   // all on their way before the first sum
 #pragma unroll
@@ -570,19 +575,14 @@ __global__ void __launch_bounds__(SH_THREADS) k_lora_few(const ShrinkArgs sp, co
     // this CTA's columns, in pairs
     const int eights = p.N / 8, c0 = 4 * static_cast<int>(static_cast<int64_t>(q) * eights / cl),
               c1 = 4 * static_cast<int>(static_cast<int64_t>(q + 1) * eights / cl);
-    const Tile t = tile_of(p, blockIdx.y);
-    {
-        int a, start, count, live;
-        shrink_tile(sp, blockIdx.y, a, start, count, live);   // reports a bad entry or rank
-    }
-    if (t.live == 0) {
-        copy_rows<YT>(p, t, q, cl);
+    ShrinkTile t;
+    if (!shrink_tile(sp, blockIdx.y, t) || t.live == 0) {
+        copy_rows<YT>(p, tile_of(p, blockIdx.y), q, cl);
         return;   // the whole cluster leaves
     }
-    if (tid < LR_TILE) {
-        const int m = tid < t.count ? p.order[t.start + tid] : -1;
-        rows[tid] = m < p.M ? m : -1;
-    }
+#pragma unroll
+    for (int j = 0; j < LR_TILE / 16; ++j)
+        if ((tid & 15) == 0) rows[(tid >> 4) + 16 * j] = t.m[j];
     const uint16_t* bcol = p.B + static_cast<int64_t>(t.a) * p.N * p.r;
     uint4 b[2][RC / 8];   // column, eight rank positions
     auto load_b = [&](int c) {
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(SH_THREADS) k_lora_few(const ShrinkArgs sp, co
                                                    : make_uint4(0u, 0u, 0u, 0u);
     };
     if constexpr (RC <= 32) load_b(c0 + tid);   // before t is formed
-    shrink_part<BF, RC>(sp, t.a, t.start, t.count, 0, t.live, q, cl, sm);
+    shrink_part<BF, RC>(sp, t, 0, t.live, q, cl, sm);
     cluster_sync();
     {
         const float scale = sp.scales != nullptr ? sp.scales[t.a] : 1.f;
