@@ -11,6 +11,8 @@
 // most 2 r flops per element of X and of Y, and X, base and Y are read or
 // written once.
 #include <cstdint>
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -422,6 +424,18 @@ constexpr int out_bytes = YT == HQ_F32 ? 4 : 2;
 __device__ __forceinline__ float2 widen16(bool bf, uint32_t w) {
     return bf ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u))
               : __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// v plus one half of a word of two 16-bit values, in fp32 (no widening first)
+template <bool BF>
+__device__ __forceinline__ float add16(uint32_t w, bool high, float v) {
+    const uint16_t h = static_cast<uint16_t>(high ? w >> 16 : w);
+    float r;
+    if constexpr (BF)
+        asm("add.rn.f32.bf16 %0, %1, %2;" : "=f"(r) : "h"(h), "f"(v));
+    else
+        asm("add.rn.f32.f16 %0, %1, %2;" : "=f"(r) : "h"(h), "f"(v));
+    return r;
 }
 
 __device__ __forceinline__ uint32_t narrow16(bool bf, float a, float b) {
@@ -881,24 +895,26 @@ __global__ void __launch_bounds__(EX_THREADS + 32, 2) k_lora_expand(const Expand
         }
     };
     const uint32_t slot0 = smem_u32(slots) + tid * 16;
-    int yleft = p.N - blk0 * EX_NB - c0 - 8 * t4;
+    int yleft = p.N - blk0 * EX_NB - c0 - 8 * t4;   // columns left for this lane
+    int64_t ybytes = 0;                              // from the first block on
+    // a warp whose rows are all there, with a base: no checks but for the last block
+    const bool whole = __all_sync(0xFFFFFFFFu, p.base != nullptr && m[0][0] >= 0 && m[0][1] >= 0 && m[1][0] >= 0 && m[1][1] >= 0);
     auto load_base = [&](bool more, int slot) {
-        if (more) {
-            const uint32_t sd = slot0 + slot * BASE;
+        if (!more) return;
+        const uint32_t sd = slot0 + slot * BASE;
+        const bool all = whole && yleft >= 64;
 #pragma unroll
-            for (int f = 0; f < 2; ++f)
+        for (int f = 0; f < 2; ++f)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (ysrc[f][h] != nullptr) {
-                        if (yleft > 0) {
+            for (int h = 0; h < 2; ++h) {
+                if (all || (ysrc[f][h] != nullptr && yleft > 0)) {
 #pragma unroll
-                            for (int e = 0; e < PIECES; ++e)
-                                cp_async16(sd + ((f * 2 + h) * PIECES + e) * EX_THREADS * 16, ysrc[f][h] + 16 * e);
-                        }
-                        ysrc[f][h] += EX_NB * ES;
-                    }
-            yleft -= EX_NB;
-        }
+                    for (int e = 0; e < PIECES; ++e)
+                        cp_async16(sd + ((f * 2 + h) * PIECES + e) * EX_THREADS * 16, ysrc[f][h] + ybytes + 16 * e);
+                }
+            }
+        ybytes += EX_NB * ES;
+        yleft -= EX_NB;
     };
     load_b();
     load_base(true, 0);
@@ -972,6 +988,7 @@ __global__ void __launch_bounds__(EX_THREADS + 32, 2) k_lora_expand(const Expand
             for (int h = 0; h < 2; ++h) us[f][h] = unscale[32 * quarter + 16 * f + 8 * h + g];
     }
     int left = p.N - blk0 * EX_NB - c0 - 8 * t4;
+    int64_t dbytes = 0;
     int slot = 0;
     for (int blk = blk0; blk < blk1; ++blk) {
         if (p.depth > 1 || blk == blk0)
@@ -994,43 +1011,48 @@ __global__ void __launch_bounds__(EX_THREADS + 32, 2) k_lora_expand(const Expand
             tmem_ld_16x256b_x4(at, acc[0]);
             tmem_ld_16x256b_x4(at + (16u << 16), acc[1]);
             tmem_wait_ld();
+            auto store = [&](auto checked) {
+                constexpr bool CHECK = decltype(checked)::value;
 #pragma unroll
-            for (int f = 0; f < 2; ++f)
+                for (int f = 0; f < 2; ++f)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (m[f][h] < 0 || left <= 0) continue;
+                    for (int h = 0; h < 2; ++h) {
+                        if (CHECK && (m[f][h] < 0 || left <= 0)) continue;
 #pragma unroll
-                    for (int e = 0; e < PIECES; ++e) {
-                        uint32_t w[4] = {0u, 0u, 0u, 0u};
-                        if (p.base != nullptr) {
-                            const uint4 y = *reinterpret_cast<const uint4*>(
-                                sd + ((f * 2 + h) * PIECES + e) * EX_THREADS * 16);
-                            w[0] = y.x; w[1] = y.y; w[2] = y.z; w[3] = y.w;
-                        }
-                        constexpr int PER = YT == HQ_F32 ? 1 : 2;   // outputs per word
+                        for (int e = 0; e < PIECES; ++e) {
+                            uint4 y = make_uint4(0u, 0u, 0u, 0u);
+                            if (!CHECK || p.base != nullptr)
+                                y = *reinterpret_cast<const uint4*>(sd + ((f * 2 + h) * PIECES + e) * EX_THREADS * 16);
+                            uint32_t w[4] = {y.x, y.y, y.z, y.w};
+                            constexpr int PER = YT == HQ_F32 ? 1 : 2;   // outputs per word
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int o = (4 * e + k) * PER;   // output 2 i + c (of 8) is acc[4 i + 2 h + c]
-                            float v0 = __uint_as_float(acc[f][4 * (o / 2) + 2 * h + (o & 1)]);
-                            if constexpr (!BF) v0 = __fmul_rn(v0, us[f][h]);
-                            if constexpr (YT == HQ_F32) {
-                                w[k] = __float_as_uint(__fadd_rn(__uint_as_float(w[k]), v0));
-                            } else {
-                                float v1 = __uint_as_float(acc[f][4 * (o / 2) + 2 * h + 1]);
-                                if constexpr (!BF) v1 = __fmul_rn(v1, us[f][h]);
-                                const float2 y = widen16(YT == HQ_BF16, w[k]);
-                                w[k] = narrow16(YT == HQ_BF16, __fadd_rn(y.x, v0), __fadd_rn(y.y, v1));
+                            for (int k = 0; k < 4; ++k) {
+                                const int o = (4 * e + k) * PER;   // output 2 i + c (of 8) is acc[4 i + 2 h + c]
+                                float v0 = __uint_as_float(acc[f][4 * (o / 2) + 2 * h + (o & 1)]);
+                                if constexpr (!BF) v0 = __fmul_rn(v0, us[f][h]);
+                                if constexpr (YT == HQ_F32) {
+                                    w[k] = __float_as_uint(__fadd_rn(__uint_as_float(w[k]), v0));
+                                } else {
+                                    float v1 = __uint_as_float(acc[f][4 * (o / 2) + 2 * h + 1]);
+                                    if constexpr (!BF) v1 = __fmul_rn(v1, us[f][h]);
+                                    w[k] = narrow16(YT == HQ_BF16, add16<YT == HQ_BF16>(w[k], false, v0),
+                                                    add16<YT == HQ_BF16>(w[k], true, v1));
+                                }
                             }
+                            reinterpret_cast<uint4*>(ydst[f][h] + dbytes)[e] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
-                        reinterpret_cast<uint4*>(ydst[f][h])[e] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    ydst[f][h] += EX_NB * ES;
-                }
+            };
+            if (whole && __all_sync(0xFFFFFFFFu, left > 0))
+                store(std::false_type{});
+            else
+                store(std::true_type{});
             load_base(blk + p.depth < blk1, slot);
         }
         cp_async_commit();
         slot = slot + 1 == p.depth ? 0 : slot + 1;
         left -= EX_NB;
+        dbytes += EX_NB * ES;
     }
     cp_async_wait_all();
     tc_fence_before();
