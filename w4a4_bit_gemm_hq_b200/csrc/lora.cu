@@ -160,6 +160,9 @@ struct ShrinkArgs {
 constexpr int SH_THREADS = 256;
 constexpr int SH_STAGES = 3;
 constexpr int SH_MAX_CL = 8;      // CTAs of a cluster, each a run of K
+// CTAs per SM that registers and shared memory are sized for
+template <int RC>
+constexpr int sh_ctas = RC == 64 ? 2 : 3;
 
 // 16-byte asynchronous copy; bytes past `bytes` (0 or 16) are written as zero
 __device__ __forceinline__ void cp_async16_z(uint32_t dst, const void* src, int bytes) {
@@ -347,7 +350,7 @@ __device__ __forceinline__ void shrink_part(const ShrinkArgs& p, const ShrinkTil
 // One tile and RC columns of the rank per cluster, CTA q a part of K; the partial
 // sums meet in a fixed order over the cluster.
 template <bool BF, int RC>
-__global__ void __launch_bounds__(SH_THREADS) k_lora_shrink(const ShrinkArgs p) {
+__global__ void __launch_bounds__(SH_THREADS, sh_ctas<RC>) k_lora_shrink(const ShrinkArgs p) {
     extern __shared__ __align__(128) uint8_t sm[];
     asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x;
@@ -581,7 +584,7 @@ constexpr int few_ring = SH_STAGES * (LR_TILE + RC) * 256 > 4 * LR_TILE * RC * 4
                                                                                  : 4 * LR_TILE * RC * 4;
 
 template <bool BF, int YT, int RC>
-__global__ void __launch_bounds__(SH_THREADS) k_lora_few(const ShrinkArgs sp, const ExpandArgs p) {
+__global__ void __launch_bounds__(SH_THREADS, RC <= 32 ? 2 : 1) k_lora_few(const ShrinkArgs sp, const ExpandArgs p) {
     extern __shared__ __align__(128) uint8_t sm[];   // the ring, later the partial sums; t [64][RC]
     __shared__ int rows[LR_TILE];
     float* tt = reinterpret_cast<float*>(sm + few_ring<RC>);
@@ -1069,7 +1072,7 @@ hq_status launch_shrink(const ShrinkArgs& a, int tiles, cudaStream_t st) {
     static SmemOptIn opt_in;
     if (!allow_smem(opt_in, kern, smem)) return HQ_ERR_CUDA;
     // K is cut as far as the GPU holds all CTAs at once
-    const int z = (a.r + RC - 1) / RC, slots = 148 * (RC == 64 ? 2 : 3);
+    const int z = (a.r + RC - 1) / RC, slots = 148 * sh_ctas<RC>;
     int cl = SH_MAX_CL;
     while (cl > 1 && static_cast<int64_t>(tiles) * z * cl > slots) cl /= 2;
     cudaLaunchConfig_t cfg = {};
