@@ -25,6 +25,9 @@ namespace {
 constexpr int LR_TILE = 64;         // tokens per tile
 constexpr int LR_MAX_ADAPTERS = 1022;   // the plan's CTA has a thread per bucket and one more
 
+// Where part q of cl (a power of two) of `n` (below 2^24) begins
+__device__ __forceinline__ int part_of(int n, int q, int cl) { return (q * n) >> (__ffs(cl) - 1); }
+
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ------------------------------------------------------------------------ plan
@@ -148,6 +151,10 @@ __global__ void __launch_bounds__(PL_THREADS) k_lora_plan(const int32_t* __restr
 }
 
 // ---------------------------------------------------------------------- shrink
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<uint64_t>(p)));
+}
+
 struct ShrinkArgs {
     const uint16_t *X, *A;
     const int32_t *order, *tiles, *ranks;
@@ -222,7 +229,7 @@ __device__ __forceinline__ bool shrink_tile(const ShrinkArgs& p, int i, ShrinkTi
         if (threadIdx.x == 0) record_status(HQ_ERR_ARG);
         return false;
     }
-    const int row = threadIdx.x >> 4;
+    const int row = threadIdx.x < SH_THREADS ? threadIdx.x >> 4 : LR_TILE;   // the others have none
 #pragma unroll
     for (int j = 0; j < LR_TILE / 16; ++j) t.m[j] = row + 16 * j < t.count ? p.order[t.start + row + 16 * j] : 0;
     t.live = p.ranks != nullptr ? p.ranks[t.a] : p.r;
@@ -246,6 +253,7 @@ __device__ __forceinline__ bool shrink_tile(const ShrinkArgs& p, int i, ShrinkTi
 // cp.async ring as two halves of 128-byte rows (16-byte chunk c of row i at
 // chunk c ^ (i & 7)).  Warp (h, w) takes 32 of the tile's tokens and channels
 // 16 w .. 16 w + 15 of each half; the warps' sums meet in a fixed order.
+// For the first SH_THREADS threads of a CTA.
 template <bool BF, int RC>
 __device__ __forceinline__ void shrink_part(const ShrinkArgs& p, const ShrinkTile& t, int r0, int live, int q, int cl,
                                             uint8_t* sm) {
@@ -261,8 +269,7 @@ __device__ __forceinline__ void shrink_part(const ShrinkArgs& p, const ShrinkTil
     const uint32_t dst = (chunk >> 3) * HALF + crow * 128 + (((chunk & 7) ^ (crow & 7)) << 4);
 
     const int slabs = (p.K + 127) / 128;
-    const int lo = static_cast<int>(static_cast<int64_t>(q) * slabs / cl);
-    const int hi = static_cast<int>(static_cast<int64_t>(q + 1) * slabs / cl);
+    const int lo = part_of(slabs, q, cl), hi = part_of(slabs, q + 1, cl);
     auto issue = [&](int s, int slot) {
         if (s < hi) {
             const int k = s * 128;
@@ -299,7 +306,7 @@ __device__ __forceinline__ void shrink_part(const ShrinkArgs& p, const ShrinkTil
     int slot = 0;
     for (int s = lo; s < hi; ++s) {
         cp_async_wait_group<SH_STAGES - 2>();
-        __syncthreads();
+        named_bar_sync(1, SH_THREADS);
         issue(s + SH_STAGES - 1, slot == 0 ? SH_STAGES - 1 : slot - 1);
         if (m0 < count) {
 #pragma unroll
@@ -324,7 +331,7 @@ __device__ __forceinline__ void shrink_part(const ShrinkArgs& p, const ShrinkTil
         slot = slot + 1 == SH_STAGES ? 0 : slot + 1;
     }
     cp_async_wait_all();
-    __syncthreads();
+    named_bar_sync(1, SH_THREADS);
 
     // ---- partial sums: [k16 warp][token][RC], then over those warps into the first
     float* part = reinterpret_cast<float*>(sm);
@@ -337,7 +344,7 @@ __device__ __forceinline__ void shrink_part(const ShrinkArgs& p, const ShrinkTil
             *reinterpret_cast<float2*>(d) = make_float2(acc[mt][i][0], acc[mt][i][1]);
             *reinterpret_cast<float2*>(d + 8 * RC) = make_float2(acc[mt][i][2], acc[mt][i][3]);
         }
-    __syncthreads();
+    named_bar_sync(1, SH_THREADS);
     float4* part4 = reinterpret_cast<float4*>(sm);
     for (int i = tid; i < count * (RC / 4); i += SH_THREADS) {
         float4 v = part4[i];
@@ -369,6 +376,7 @@ __global__ void __launch_bounds__(SH_THREADS, sh_ctas<RC>) k_lora_shrink(const S
     }
 
     shrink_part<BF, RC>(p, t, r0, live, q, cl, sm);
+    __syncthreads();
     const float4* part4 = reinterpret_cast<const float4*>(sm);
     cluster_sync();
     const float scale = p.scales != nullptr ? p.scales[t.a] : 1.f;
@@ -458,7 +466,7 @@ __device__ void copy_cols(const ExpandArgs& p, const Tile& t, int col0, int cols
 template <int YT>
 __device__ void copy_rows(const ExpandArgs& p, const Tile& t, int q, int cl) {
     const int eights = p.N / 8;
-    const int a = static_cast<int>(static_cast<int64_t>(q) * eights / cl), b = static_cast<int>(static_cast<int64_t>(q + 1) * eights / cl);
+    const int a = part_of(eights, q, cl), b = part_of(eights, q + 1, cl);
     copy_cols<YT>(p, t, 8 * a, 8 * (b - a));
 }
 
@@ -572,34 +580,38 @@ __global__ void __launch_bounds__(FEW_THREADS) k_lora_expand_few(const ExpandArg
 }
 
 // Few tokens per tile, both products in one launch: a cluster of 8 CTAs forms a
-// tile's t (each a part of K), every CTA reads the partial sums of all of them
-// from their shared memory, and then each takes an eighth of the columns, as in
-// k_lora_expand_few, two neighbouring ones a thread, with the next pair's B and
-// base loaded a round ahead.  Ranks up to 64; t has no place in memory.  Against
-// the two kernels it takes 1 us longer on the GPU but 2.5 us less of the host,
-// which is what a single step waits for.  (Staging all of the CTA's B by bulk
-// copies of one pair of rows each took 3 us more: they are too small.)
+// tile's t (each a part of K, by its first 256 threads), every CTA reads the
+// partial sums of all of them from their shared memory, and then each takes an
+// eighth of the columns, two neighbouring ones a thread, in plain fp32.  Bound by
+// the latency of its chain of loads and barriers: threads of their own load their
+// columns' B and the first token's base while t is formed, those that form it
+// have theirs prefetched into L2.  Ranks up to 64; t has no place in memory.
+// Against the two kernels: one launch less of host time (2.5 us), which is what a
+// single step waits for.
+template <int RC>
+constexpr int few_threads = RC <= 32 ? 768 : 512;
 template <int RC>
 constexpr int few_ring = SH_STAGES * (LR_TILE + RC) * 256 > 4 * LR_TILE * RC * 4 ? SH_STAGES * (LR_TILE + RC) * 256
                                                                                  : 4 * LR_TILE * RC * 4;
 
 template <bool BF, int YT, int RC>
-__global__ void __launch_bounds__(SH_THREADS, RC <= 32 ? 2 : 1) k_lora_few(const ShrinkArgs sp, const ExpandArgs p) {
+__global__ void __launch_bounds__(few_threads<RC>) k_lora_few(const ShrinkArgs sp, const ExpandArgs p) {
     extern __shared__ __align__(128) uint8_t sm[];   // the ring, later the partial sums; t [64][RC]
     __shared__ int rows[LR_TILE];
+    constexpr int THREADS = few_threads<RC>;
     float* tt = reinterpret_cast<float*>(sm + few_ring<RC>);
     const int tid = threadIdx.x, q = blockIdx.x, cl = gridDim.x;
-    // this CTA's columns, in pairs
-    const int eights = p.N / 8, c0 = 4 * static_cast<int>(static_cast<int64_t>(q) * eights / cl),
-              c1 = 4 * static_cast<int>(static_cast<int64_t>(q + 1) * eights / cl);
+    const int c0 = 4 * part_of(p.N / 8, q, cl), c1 = 4 * part_of(p.N / 8, q + 1, cl);   // this CTA's pairs of columns
     ShrinkTile t;
     if (!shrink_tile(sp, blockIdx.y, t) || t.live == 0) {
         copy_rows<YT>(p, tile_of(p, blockIdx.y), q, cl);
         return;   // the whole cluster leaves
     }
+    if (tid < SH_THREADS) {
 #pragma unroll
-    for (int j = 0; j < LR_TILE / 16; ++j)
-        if ((tid & 15) == 0) rows[(tid >> 4) + 16 * j] = t.m[j];
+        for (int j = 0; j < LR_TILE / 16; ++j)
+            if ((tid & 15) == 0) rows[(tid >> 4) + 16 * j] = t.m[j];
+    }
     const uint16_t* bcol = p.B + static_cast<int64_t>(t.a) * p.N * p.r;
     uint4 b[2][RC / 8];   // column, eight rank positions
     auto load_b = [&](int c) {
@@ -611,21 +623,41 @@ __global__ void __launch_bounds__(SH_THREADS, RC <= 32 ? 2 : 1) k_lora_few(const
                 b[k][e] = c < c1 && 8 * e < t.live ? __ldg(reinterpret_cast<const uint4*>(s + k * p.r) + e)
                                                    : make_uint4(0u, 0u, 0u, 0u);
     };
-    if constexpr (RC <= 32) load_b(c0 + tid);   // before t is formed
-    shrink_part<BF, RC>(sp, t, 0, t.live, q, cl, sm);
+    auto base_at = [&](int m, int c) {
+        if (p.base == nullptr || m < 0 || c >= c1) return make_float2(0.f, 0.f);
+        const uint8_t* s = static_cast<const uint8_t*>(p.base) + (m * p.ldb + 2 * c) * out_bytes<YT>;
+        return YT == HQ_F32 ? *reinterpret_cast<const float2*>(s) : widen16(YT == HQ_BF16, *reinterpret_cast<const uint32_t*>(s));
+    };
+    // the threads that do not form t have the first pairs
+    const int first = c0 + (tid < SH_THREADS ? tid + THREADS - SH_THREADS : tid - SH_THREADS);
+    float2 ynext = make_float2(0.f, 0.f);
+    if (tid < SH_THREADS) {
+        shrink_part<BF, RC>(sp, t, 0, t.live, q, cl, sm);
+    } else {
+        load_b(first);
+        int m0 = p.order[t.start];
+        ynext = base_at(m0 < p.M ? m0 : -1, first);
+        // everything else of this CTA's B
+        const int64_t bytes = static_cast<int64_t>(c1 - c0) * 4 * p.r;
+        const uint8_t* s = reinterpret_cast<const uint8_t*>(bcol + static_cast<int64_t>(2 * c0) * p.r);
+        for (int64_t o = static_cast<int64_t>(THREADS - SH_THREADS) * 4 * p.r + (tid - SH_THREADS) * 128; o < bytes;
+             o += (THREADS - SH_THREADS) * 128)
+            prefetch_l2(s + o);
+    }
     cluster_sync();
     {
         const float scale = sp.scales != nullptr ? sp.scales[t.a] : 1.f;
         const float4* part4 = reinterpret_cast<const float4*>(sm);
-        for (int i = tid; i < t.count * (RC / 4); i += SH_THREADS) {
-            float4 u[SH_MAX_CL];
+        for (int i = tid; i < t.count * (RC / 4); i += THREADS) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int c = 0; c < SH_MAX_CL; ++c)
-                if (c < cl) u[c] = ld_cluster_f32x4(mapa_shared(smem_u32(part4 + i), c));
-            float4 v = u[0];
+            for (int h = 0; h < SH_MAX_CL; h += 4) {   // four on their way before they are added
+                float4 u[4];
 #pragma unroll
-            for (int c = 1; c < SH_MAX_CL; ++c)
-                if (c < cl) v = add4(v, u[c]);
+                for (int c = 0; c < 4; ++c) u[c] = ld_cluster_f32x4(mapa_shared(smem_u32(part4 + i), h + c));
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v = add4(v, u[c]);
+            }
             const int col = i % (RC / 4) * 4;
             v.x = col < t.live ? __fmul_rn(v.x, scale) : 0.f;
             v.y = col + 1 < t.live ? __fmul_rn(v.y, scale) : 0.f;
@@ -634,53 +666,52 @@ __global__ void __launch_bounds__(SH_THREADS, RC <= 32 ? 2 : 1) k_lora_few(const
             reinterpret_cast<float4*>(tt)[i] = v;
         }
     }
-    // base of the first token and pair, then a pair ahead
-    auto base_at = [&](int m, int c) {
-        if (p.base == nullptr || m < 0 || c >= c1) return make_float2(0.f, 0.f);
-        const uint8_t* s = static_cast<const uint8_t*>(p.base) + (m * p.ldb + 2 * c) * out_bytes<YT>;
-        return YT == HQ_F32 ? *reinterpret_cast<const float2*>(s) : widen16(YT == HQ_BF16, *reinterpret_cast<const uint32_t*>(s));
-    };
-    float2 ynext = base_at(rows[0], c0 + tid);
-    cluster_sync();   // t is there, and nobody reads another CTA's sums any more
-    if constexpr (RC > 32) load_b(c0 + tid);
-    for (int c = c0 + tid; c < c1; c += SH_THREADS) {
-        float w[2][RC];
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int e = 0; e < RC / 8; ++e) {
-                const uint32_t x[4] = {b[k][e].x, b[k][e].y, b[k][e].z, b[k][e].w};
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const float2 f = widen16(BF, x[u]);
-                    // past the adapter's rank B is not read as a number
-                    w[k][8 * e + 2 * u] = 8 * e + 2 * u < t.live ? f.x : 0.f;
-                    w[k][8 * e + 2 * u + 1] = 8 * e + 2 * u + 1 < t.live ? f.y : 0.f;
-                }
-            }
-        load_b(c + SH_THREADS);
+    // this CTA has read the others' sums; they may leave once all have (the wait is at the end)
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    __syncthreads();   // t is there
+    if (tid < SH_THREADS) {
+        load_b(first);
+        ynext = base_at(rows[0], first);
+    }
+    for (int c = first; c < c1; c += THREADS) {
+        if (c != first) {
+            load_b(c);
+            ynext = base_at(rows[0], c);
+        }
         for (int i = 0; i < t.count; ++i) {
             const int m = rows[i];
             const float2 y = ynext;
-            ynext = i + 1 < t.count ? base_at(rows[i + 1], c) : base_at(rows[0], c + SH_THREADS);
+            if (i + 1 < t.count) ynext = base_at(rows[i + 1], c);
             if (m < 0) continue;
             float acc[2] = {0.f, 0.f};
 #pragma unroll
-            for (int j = 0; j < RC; j += 4) {
-                const float4 v = *reinterpret_cast<const float4*>(tt + i * RC + j);
+            for (int e = 0; e < RC / 8; ++e) {
+                if (8 * e >= t.live) break;
+                const float4 v0 = *reinterpret_cast<const float4*>(tt + i * RC + 8 * e);
+                const float4 v1 = *reinterpret_cast<const float4*>(tt + i * RC + 8 * e + 4);
+                const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    acc[k] = __fmaf_rn(v.w, w[k][j + 3],
-                                       __fmaf_rn(v.z, w[k][j + 2], __fmaf_rn(v.y, w[k][j + 1], __fmaf_rn(v.x, w[k][j], acc[k]))));
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t x[4] = {b[k][e].x, b[k][e].y, b[k][e].z, b[k][e].w};
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        asm volatile("" : "+r"(x[u]));   // widened per token: kept widened, B would not fit the registers
+                        const float2 f = widen16(BF, x[u]);
+                        // past the adapter's rank B is not read as a number
+                        acc[k] = __fmaf_rn(v[2 * u], 8 * e + 2 * u < t.live ? f.x : 0.f, acc[k]);
+                        acc[k] = __fmaf_rn(v[2 * u + 1], 8 * e + 2 * u + 1 < t.live ? f.y : 0.f, acc[k]);
+                    }
+                }
             }
             uint8_t* d = static_cast<uint8_t*>(p.Y) + (m * p.ldy + 2 * c) * out_bytes<YT>;
-            const float v0 = __fadd_rn(y.x, acc[0]), v1 = __fadd_rn(y.y, acc[1]);
+            const float r0 = __fadd_rn(y.x, acc[0]), r1 = __fadd_rn(y.y, acc[1]);
             if constexpr (YT == HQ_F32)
-                *reinterpret_cast<float2*>(d) = make_float2(v0, v1);
+                *reinterpret_cast<float2*>(d) = make_float2(r0, r1);
             else
-                *reinterpret_cast<uint32_t*>(d) = narrow16(YT == HQ_BF16, v0, v1);
+                *reinterpret_cast<uint32_t*>(d) = narrow16(YT == HQ_BF16, r0, r1);
         }
     }
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Whole tiles (prompts): t of two tiles (128 tokens) and blocks of 64 rows of B
@@ -1141,7 +1172,7 @@ hq_status launch_few(const ShrinkArgs& s, const ExpandArgs& e, int tiles, cudaSt
     if (!allow_smem(opt_in, kern, smem)) return HQ_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(SH_MAX_CL, tiles);
-    cfg.blockDim = dim3(SH_THREADS);
+    cfg.blockDim = dim3(few_threads<RC>);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
