@@ -253,8 +253,9 @@ __device__ __forceinline__ bool shrink_tile(const ShrinkArgs& p, int i, ShrinkTi
 // cp.async ring as two halves of 128-byte rows (16-byte chunk c of row i at
 // chunk c ^ (i & 7)).  Warp (h, w) takes 32 of the tile's tokens and channels
 // 16 w .. 16 w + 15 of each half; the warps' sums meet in a fixed order.
-// For the first SH_THREADS threads of a CTA.
-template <bool BF, int RC>
+// For the first SH_THREADS threads of a CTA; the others of `ALL` wait on barrier 2
+// until the first stages have been asked for.
+template <bool BF, int RC, int ALL>
 __device__ __forceinline__ void shrink_part(const ShrinkArgs& p, const ShrinkTile& t, int r0, int live, int q, int cl,
                                             uint8_t* sm) {
     constexpr int HALF = (LR_TILE + RC) * 128, STAGE = 2 * HALF;
@@ -303,6 +304,7 @@ __device__ __forceinline__ void shrink_part(const ShrinkArgs& p, const ShrinkTil
     const uint32_t aoff = (m0 + am) * 128 + ((ac ^ (am & 7)) << 4);
     const uint32_t boff = LR_TILE * 128 + bn * 128 + ((bc ^ (bn & 7)) << 4);
     for (int s = 0; s < SH_STAGES - 1; ++s) issue(lo + s, s);
+    if constexpr (ALL > SH_THREADS) asm volatile("bar.arrive 2, %0;" ::"n"(ALL) : "memory");
     int slot = 0;
     for (int s = lo; s < hi; ++s) {
         cp_async_wait_group<SH_STAGES - 2>();
@@ -375,7 +377,7 @@ __global__ void __launch_bounds__(SH_THREADS, sh_ctas<RC>) k_lora_shrink(const S
         return;
     }
 
-    shrink_part<BF, RC>(p, t, r0, live, q, cl, sm);
+    shrink_part<BF, RC, SH_THREADS>(p, t, r0, live, q, cl, sm);
     __syncthreads();
     const float4* part4 = reinterpret_cast<const float4*>(sm);
     cluster_sync();
@@ -632,10 +634,11 @@ __global__ void __launch_bounds__(few_threads<RC>) k_lora_few(const ShrinkArgs s
     const int first = c0 + (tid < SH_THREADS ? tid + THREADS - SH_THREADS : tid - SH_THREADS);
     float2 ynext = make_float2(0.f, 0.f);
     if (tid < SH_THREADS) {
-        shrink_part<BF, RC>(sp, t, 0, t.live, q, cl, sm);
+        shrink_part<BF, RC, THREADS>(sp, t, 0, t.live, q, cl, sm);
     } else {
+        const int m0 = p.order[t.start];
+        named_bar_sync(2, THREADS);   // X and A first: t waits for them
         load_b(first);
-        int m0 = p.order[t.start];
         ynext = base_at(m0 < p.M ? m0 : -1, first);
         // everything else of this CTA's B
         const int64_t bytes = static_cast<int64_t>(c1 - c0) * 4 * p.r;
