@@ -527,7 +527,8 @@ hq_status hq_mxfp4_linear(const uint8_t* Xq, const uint8_t* sx, int64_t M, int64
  *   p = fl(gate * p)                                   (gate given)
  *   h = e(fl(H + fl(alpha * p)))                       (h = H when Y is NULL)
  *   X = e(fl(fl(h * fl(w + w_offset)) * r(h)))         (w given)
- * with r(v) = 1 / sqrt(sum v^2 / K + eps), the sum in fp32 (|v| below 1e18).
+ * with r(v) = 1 / sqrt(sum v^2 / K + eps), the sum in fp32 (|v| below 1e18; eps = 0
+ * makes X NaN where a row is zero).
  *  H        device, [M][ld_h] residual stream
  *  Y        device, [M][ld_y] the block's output, or NULL (no block: H is normed)
  *  xt       type of H, Y, gate, H_out and X: HQ_F16, HQ_BF16 or HQ_F32
@@ -587,8 +588,9 @@ hq_status hq_norm_rotate_quant(const void* H, int64_t ld_h, const void* Y, int64
  *  tiles  device, [hq_lora_max_tiles(M, n)][3] int32 (output): `order` cut into
  *         runs of at most 64 tokens of one id: (id, first position, tokens), in
  *         order; unused entries are (-1, 0, 0)
- * Errors: HQ_ERR_ARG (M < 0, n < 0, NULL with M > 0), HQ_ERR_UNSUPPORTED (n > 1022,
- * more than 65535 tiles), HQ_ERR_CUDA.  M == 0 is a no-op.
+ * Errors: HQ_ERR_ARG (M < 0, n < 0, NULL with M > 0, one buffer given twice),
+ * HQ_ERR_UNSUPPORTED (n > 1022, more than 65535 tiles), HQ_ERR_CUDA.  M == 0 is a
+ * no-op.
  */
 int64_t hq_lora_max_tiles(int64_t M, int64_t n);
 hq_status hq_lora_plan(const int32_t* ids, int64_t M, int64_t n, int32_t* order, int32_t* tiles, void* stream);

@@ -79,8 +79,9 @@ def test_max_tiles_is_enough_for_any_batch(lib, M, n):
 
 
 @pytest.mark.parametrize("a,want", [
-    ((P, -1, 4, P, P), ARG), ((P, 8, -1, P, P), ARG), ((None, 8, 4, P, P), ARG), ((P, 8, 4, None, P), ARG),
-    ((P, 8, 4, P, None), ARG), ((P, 8, 1023, P, P), UNSUPPORTED), ((P, 1 << 23, 4, P, P), UNSUPPORTED),
+    ((P, -1, 4, P2, P3), ARG), ((P, 8, -1, P2, P3), ARG), ((None, 8, 4, P2, P3), ARG), ((P, 8, 4, None, P3), ARG),
+    ((P, 8, 4, P2, None), ARG), ((P, 8, 1023, P2, P3), UNSUPPORTED), ((P, 1 << 23, 4, P2, P3), UNSUPPORTED),
+    ((P, 8, 4, P, P3), ARG), ((P, 8, 4, P2, P), ARG), ((P, 8, 4, P2, P2), ARG),
     ((None, 0, 4, None, None), OK),
 ])
 def test_plan_refusals(lib, a, want):

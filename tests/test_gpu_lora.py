@@ -272,8 +272,31 @@ def test_bad_plans_are_not_read_through():
         assert (out[first] == 9).all()
 
 
-def test_ranks_outside_are_clamped_and_reported():
-    d = batch(20, 64, 64, 2, 8, F16, F16, ragged=False, bare=False)
+def test_bad_plans_of_whole_tiles():
+    M = 400
+    d = batch(M, 128, 72, 3, 16, F16, F16, ragged=False, runs=40, bare=False)
+    order, tiles = hq.hq_lora_plan(d["ids"], 3)
+    want = apply(d, (order, tiles))
+    bad = order.clone()
+    bad[0], bad[M - 1] = -5, 1 << 30
+    out = torch.full((M, 72), 9.0, dtype=F16, device="cuda")
+    apply(d, (bad, tiles), Y=out)
+    assert hq.hq_last_device_status() == 1
+    keep = torch.ones(M, dtype=torch.bool, device="cuda")
+    keep[order[0].long()] = keep[order[M - 1].long()] = False
+    assert torch.equal(out[keep], want[keep]) and (out[~keep] == 9).all()
+    others = d["ids"] != int(tiles[0, 0])
+    for entry in ([7, 0, 64], [0, M - 1, 2], [0, -1, 4], [1, 0, 65], [1, 5, -3], [2, 2 ** 31 - 1, 64]):
+        bad = tiles.clone()
+        bad[0] = torch.tensor(entry, dtype=torch.int32)
+        apply(d, (order, bad), Y=out)
+        assert hq.hq_last_device_status() == 1, entry
+        assert torch.equal(out[others], want[others])
+
+
+@pytest.mark.parametrize("M", [20, 300])
+def test_ranks_outside_are_clamped_and_reported(M):
+    d = batch(M, 64, 64, 2, 8, F16, F16, ragged=False, bare=False)
     want = apply(d)
     d["ranks"] = torch.tensor([100, 8], dtype=torch.int32, device="cuda")
     assert torch.equal(apply(d), want)

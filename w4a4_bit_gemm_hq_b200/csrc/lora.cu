@@ -1222,7 +1222,7 @@ extern "C" hq_status hq_lora_plan(const int32_t* ids, int64_t M, int64_t n, int3
     if (M < 0 || n < 0) return HQ_ERR_ARG;
     if (n > LR_MAX_ADAPTERS || hq_lora_max_tiles(M, n) > 65535) return HQ_ERR_UNSUPPORTED;
     if (M == 0) return HQ_OK;
-    if (!ids || !order || !tiles) return HQ_ERR_ARG;
+    if (!ids || !order || !tiles || ids == order || ids == tiles || order == tiles) return HQ_ERR_ARG;
     int cl = 1;
     while (cl < PL_MAX_CL && M > static_cast<int64_t>(PL_RUN) * cl) cl *= 2;
     // a warp per 32 tokens, up to a full CTA
