@@ -4,7 +4,7 @@ the fp32 sequence that defines them, in numpy).
 
 Tolerances, u = 2^-24 (half a step of fp32):
  * a row's sum of squares: at most 32 sequential fused adds per thread, 5 over
-   the lanes and 16 over the warps, all terms positive: relative 53 u; the mean's
+   the lanes and up to 16 over the warps, all terms positive: relative 53 u; the mean's
    division, the added eps, the square root and the reciprocal: 1 / sqrt is off
    by at most (53 + 1 + 1) / 2 + 1 = 28.5 u, taken as 30 u.
  * h: the block term has up to five roundings more (w + off, two products,

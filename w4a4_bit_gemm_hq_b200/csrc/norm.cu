@@ -183,23 +183,36 @@ __device__ __forceinline__ void ld_weight(const void* w, int wt, int i, int n, f
 struct RowReduce {
     float2 (*buf)[32];
     int par;
-    // (sum of s, max of a) over the CTA
-    __device__ __forceinline__ float2 operator()(float s, float a) {
+    __device__ __forceinline__ static float lanes(float s) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, s, o));
-        // a is not negative: its bits are ordered as it is
-        a = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(a)));
-        const int nw = blockDim.x >> 5;
-        if (nw > 1) {
+        return s;
+    }
+    // a is not negative: its bits are ordered as it is
+    __device__ __forceinline__ static float lanes_max(float a) {
+        return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(a)));
+    }
+    // the sum of s over the CTA; every warp adds the warps' sums for itself
+    __device__ __forceinline__ float sum(float s) {
+        s = lanes(s);
+        if (blockDim.x > 32) {
+            if ((threadIdx.x & 31) == 0) buf[par][threadIdx.x >> 5].x = s;
+            __syncthreads();
+            s = lanes((threadIdx.x & 31) < blockDim.x >> 5 ? buf[par][threadIdx.x & 31].x : 0.f);
+            par ^= 1;
+        }
+        return s;
+    }
+    // (sum of s, max of a)
+    __device__ __forceinline__ float2 sum_max(float s, float a) {
+        s = lanes(s);
+        a = lanes_max(a);
+        if (blockDim.x > 32) {
             if ((threadIdx.x & 31) == 0) buf[par][threadIdx.x >> 5] = make_float2(s, a);
             __syncthreads();
-            s = 0.f;
-            a = 0.f;
-            for (int w = 0; w < nw; ++w) {
-                const float2 t = buf[par][w];
-                s = __fadd_rn(s, t.x);
-                a = fmaxf(a, t.y);
-            }
+            const float2 t = (threadIdx.x & 31) < blockDim.x >> 5 ? buf[par][threadIdx.x & 31] : make_float2(0.f, 0.f);
+            s = lanes(t.x);
+            a = lanes_max(t.y);
             par ^= 1;
         }
         return make_float2(s, a);
@@ -214,29 +227,30 @@ __device__ __forceinline__ float inv_rms(float sum, int K, float eps) {
 // A CTA walks rows m, m + grid, ...; NV vectors per thread, vector i of thread t
 // at i * threads + t.  Bound by HBM: the weights stay in registers as fp32 over
 // the CTA's rows (KEEP) and the next row is requested before this one is worked
-// on; rows whose registers do not allow both (fp32, very wide ones) do neither,
-// other CTAs cover their waits.  A row is in registers from its load to its stores.
+// on; rows whose registers do not allow both (fp32, very wide ones) have the
+// weights in shared memory and request the next row at the end of this one.  A row is in registers from its load to its stores.
 template <int XT, int NV, bool POST, bool KEEP, bool TAIL, int MAXT>
 __global__ void __launch_bounds__(MAXT, !KEEP && MAXT == 512 ? 2 : 1) k_residual_norm(const NormArgs a) {
     constexpr int V = vec_len<XT>;
     __shared__ float2 red[2][32];
+    extern __shared__ __align__(16) float wsm[];   // weights (not KEEP)
     RowReduce reduce{red, 0};
     int n[NV];
     uint32_t col[NV], at[NV];   // first channel of a vector, its byte
-    float wp[KEEP && POST ? NV : 1][V], wn[KEEP ? NV : 1][V];
+    float wp[KEEP && POST ? NV : 1][V], wn[KEEP ? NV : 1][V];   // else of the vector at hand
     struct Row {
         uint4 h[NV], y[NV], g[NV];
     } r[KEEP ? 2 : 1];
-    auto load = [&](int64_t m, Row& q) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) q.h[i] = ld_vec<XT, TAIL>(row_of<XT>(a.H, m, a.ldh), at[i], n[i]);
+    auto load = [&](int64_t m, Row& q) {   // the block first: its norm is the first thing needed
         if (a.Y != nullptr) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) q.y[i] = ld_vec<XT, TAIL>(row_of<XT>(a.Y, m, a.ldy), at[i], n[i]);
-            if (a.gate != nullptr) {
+        }
 #pragma unroll
-                for (int i = 0; i < NV; ++i) q.g[i] = ld_vec<XT, TAIL>(row_of<XT>(a.gate, m, a.ldg), at[i], n[i]);
-            }
+        for (int i = 0; i < NV; ++i) q.h[i] = ld_vec<XT, TAIL>(row_of<XT>(a.H, m, a.ldh), at[i], n[i]);
+        if (a.Y != nullptr && a.gate != nullptr) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) q.g[i] = ld_vec<XT, TAIL>(row_of<XT>(a.gate, m, a.ldg), at[i], n[i]);
         }
     };
 #pragma unroll
@@ -246,6 +260,33 @@ __global__ void __launch_bounds__(MAXT, !KEEP && MAXT == 512 ? 2 : 1) k_residual
         n[i] = min(max(a.K - static_cast<int>(col[i]), 0), V);
     }
     load(blockIdx.x, r[0]);
+    // without registers for them the weights lie in shared memory, as fp32, in slots
+    // of 16 bytes that only their thread uses: w_post's, then w's, V / 4 per vector
+    const uint32_t slots = NV * blockDim.x;
+    auto slot = [&](int which, int i, int h) {
+        return wsm + ((which * (V / 4) + h) * slots + i * blockDim.x + threadIdx.x) * 4;
+    };
+    auto stage_w = [&](int which, const void* w) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float f[V];
+            ld_weight<V>(w, a.wt, col[i], n[i], a.off, f);
+#pragma unroll
+            for (int h = 0; h < V / 4; ++h)
+                *reinterpret_cast<float4*>(slot(which, i, h)) = make_float4(f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]);
+        }
+    };
+    auto weight = [&](int which, int i, float (&f)[V]) {
+#pragma unroll
+        for (int h = 0; h < V / 4; ++h) {
+            const float4 q = *reinterpret_cast<const float4*>(slot(which, i, h));
+            f[4 * h] = q.x; f[4 * h + 1] = q.y; f[4 * h + 2] = q.z; f[4 * h + 3] = q.w;
+        }
+    };
+    if constexpr (!KEEP) {
+        if constexpr (POST) stage_w(1, a.w_post);
+        if (a.w != nullptr) stage_w(0, a.w);
+    }
     if constexpr (KEEP) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -269,7 +310,7 @@ __global__ void __launch_bounds__(MAXT, !KEEP && MAXT == 512 ? 2 : 1) k_residual
 #pragma unroll
                     for (int e = 0; e < V; ++e) ss = __fmaf_rn(y[e], y[e], ss);
                 }
-                rstd = inv_rms(reduce(ss, 0.f).x, a.K, a.eps);
+                rstd = inv_rms(reduce.sum(ss), a.K, a.eps);
             }
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -277,7 +318,7 @@ __global__ void __launch_bounds__(MAXT, !KEEP && MAXT == 512 ? 2 : 1) k_residual
                 widen<XT>(q.y[i], p);
                 widen<XT>(q.h[i], h);
                 if constexpr (POST) {
-                    if constexpr (!KEEP) ld_weight<V>(a.w_post, a.wt, col[i], n[i], a.off, wp[0]);
+                    if constexpr (!KEEP) weight(1, i, wp[0]);
 #pragma unroll
                     for (int e = 0; e < V; ++e) p[e] = __fmul_rn(__fmul_rn(p[e], wp[KEEP ? i : 0][e]), rstd);
                 }
@@ -305,12 +346,12 @@ __global__ void __launch_bounds__(MAXT, !KEEP && MAXT == 512 ? 2 : 1) k_residual
 #pragma unroll
                 for (int e = 0; e < V; ++e) ss = __fmaf_rn(h[e], h[e], ss);
             }
-            const float rstd = inv_rms(reduce(ss, 0.f).x, a.K, a.eps);
+            const float rstd = inv_rms(reduce.sum(ss), a.K, a.eps);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 float h[V];
                 widen<XT>(q.h[i], h);
-                if constexpr (!KEEP) ld_weight<V>(a.w, a.wt, col[i], n[i], a.off, wn[0]);
+                if constexpr (!KEEP) weight(0, i, wn[0]);
 #pragma unroll
                 for (int e = 0; e < V; ++e) h[e] = __fmul_rn(__fmul_rn(h[e], wn[KEEP ? i : 0][e]), rstd);
                 st_vec<XT, TAIL>(row_of<XT>(a.X, m, a.ldx), at[i], n[i], narrow<XT>(h));
@@ -513,7 +554,7 @@ __global__ void __launch_bounds__(NM_MAXK / NQ_SPAN * 32) k_norm_quant(const Nor
         }
         if (m + gridDim.x < a.M) load(m + gridDim.x, r);   // arrives while this row is rotated
         if (a.X != nullptr) {
-            const float rstd = inv_rms(reduce(ss, 0.f).x, a.K, a.eps);
+            const float rstd = inv_rms(reduce.sum(ss), a.K, a.eps);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (on[i]) {
@@ -566,7 +607,7 @@ __global__ void __launch_bounds__(NM_MAXK / NQ_SPAN * 32) k_norm_quant(const Nor
 #pragma unroll
         for (int k = 0; k < 32; k += 2) amax[(k >> 1) & 3] = max3_abs(amax[(k >> 1) & 3], v[k], v[k + 1]);
         // ---- row scale; back to layout A
-        const float2 t = reduce(ss, fmaxf(fmaxf(amax[0], amax[1]), fmaxf(amax[2], amax[3])));
+        const float2 t = reduce.sum_max(ss, fmaxf(fmaxf(amax[0], amax[1]), fmaxf(amax[2], amax[3])));
         if (G > 8) {
             __syncwarp();   // one warp per row: the reduction has no barrier
 #pragma unroll
@@ -652,10 +693,12 @@ hq_status launch_norm(const NormArgs& a, cudaStream_t st) {
                       : k_residual_norm<XT, NW, P, false, false, 1024>;
     };
     auto kern = a.w_post != nullptr ? pick(std::true_type{}) : pick(std::false_type{});
-    // rows of their own for CTAs that keep nothing from one to the next
-    const unsigned grid = KEEP && small ? grid_for(kern, threads, 0, a.M) : static_cast<unsigned>(a.M);
+    const int smem = KEEP && small ? 0 : (a.w_post != nullptr ? 2 : 1) * nv * threads * V * 4;
+    static SmemOptIn opt_in[8];
+    if (!allow_smem(opt_in[(small ? 1 : 0) + (tail ? 2 : 0) + (a.w_post != nullptr ? 4 : 0)], kern, smem)) return HQ_ERR_CUDA;
+    const unsigned grid = grid_for(kern, threads, smem, a.M);
     if (grid == 0) return HQ_ERR_CUDA;
-    kern<<<grid, threads, 0, st>>>(a);
+    kern<<<grid, threads, smem, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
 }
 
