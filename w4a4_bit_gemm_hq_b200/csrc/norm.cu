@@ -44,6 +44,7 @@ struct NormArgs {
     int64_t ldh, ldy, ldg, ldho, ldx;
     int M, K, group, wt;
     float alpha, off, eps, cg;
+    float2 nz;   // (-0, -0)
 };
 
 // A vector is 16 bytes of the stream: 8 values of 16 bits or 4 of fp32
@@ -408,6 +409,22 @@ __device__ __forceinline__ float2 f2_sub(float2 a, float2 b) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(-1.0f));
     return r;
 }
+__device__ __forceinline__ float2 f2_fma(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+// a b, rounded on its own: the compiler merges a packed product, or one that it sees
+// to be plus -0, with a packed sum after it, so `nz` is a -0 that it does not know
+__device__ __forceinline__ float2 f2_mul(float2 a, float2 b, float2 nz) { return f2_fma(a, b, nz); }
+__device__ __forceinline__ float2 f2_of(const float* v) { return make_float2(v[0], v[1]); }
+__device__ __forceinline__ void f2_to(float* v, float2 a) {
+    v[0] = a.x;
+    v[1] = a.y;
+}
 __device__ __forceinline__ float max3_abs(float a, float b, float c) {
     float r;
     asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -491,7 +508,7 @@ __global__ void __launch_bounds__(NM_MAXK / NQ_SPAN * 32) k_norm_quant(const Nor
     };
     load(blockIdx.x, r);
     // weights of this lane's channels (each lane reads back what it wrote), and the
-    // signs of d, bit 8 i + e
+    // signs of d: those of pair 4 i + e / 2 in bits 15 and 31 less the pair's number
     uint32_t neg = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -503,7 +520,7 @@ __global__ void __launch_bounds__(NM_MAXK / NQ_SPAN * 32) k_norm_quant(const Nor
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     if (d[e] == -1) {
-                        neg |= 1u << (8 * i + e);
+                        neg |= 1u << (((e & 1) ? 31 : 15) - 4 * i - e / 2);
                         w[e] = -w[e];
                     }
             }
@@ -524,7 +541,7 @@ __global__ void __launch_bounds__(NM_MAXK / NQ_SPAN * 32) k_norm_quant(const Nor
     for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
         // ---- the residual stream after the block, v = h (w + off) d
         float v[32];
-        float ss = 0.f;
+        float2 ss2 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float h[8];
@@ -536,10 +553,11 @@ __global__ void __launch_bounds__(NM_MAXK / NQ_SPAN * 32) k_norm_quant(const Nor
                     float g[8];
                     widen<XT>(ld_vec<XT, false>(row_of<XT>(a.gate, m, a.ldg), at0 + 512 * i, 1), g);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) p[e] = __fmul_rn(g[e], p[e]);
+                    for (int e = 0; e < 8; e += 2) f2_to(p + e, f2_mul(f2_of(g + e), f2_of(p + e), a.nz));
                 }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) h[e] = __fadd_rn(h[e], __fmul_rn(a.alpha, p[e]));
+                for (int e = 0; e < 8; e += 2)
+                    f2_to(h + e, f2_add(f2_of(h + e), f2_mul(make_float2(a.alpha, a.alpha), f2_of(p + e), a.nz)));
                 r.h[i] = narrow<XT>(h);
                 widen<XT>(r.h[i], h);   // what the norm reads is the stored stream
             }
@@ -549,15 +567,16 @@ __global__ void __launch_bounds__(NM_MAXK / NQ_SPAN * 32) k_norm_quant(const Nor
                 const float4 w1 = *reinterpret_cast<const float4*>(wrow + 256 * i + 128);
                 const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    ss = __fmaf_rn(h[e], h[e], ss);
-                    v[8 * i + e] = __fmul_rn(h[e], w[e]);
+                for (int e = 0; e < 8; e += 2) {
+                    ss2 = f2_fma(f2_of(h + e), f2_of(h + e), ss2);
+                    f2_to(v + 8 * i + e, f2_mul(f2_of(h + e), f2_of(w + e), a.nz));
                 }
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[8 * i + e] = 0.f;
             }
         }
+        const float ss = __fadd_rn(ss2.x, ss2.y);
         if (m + gridDim.x < a.M) load(m + gridDim.x, r);   // arrives while this row is rotated
         if (a.X != nullptr) {
             const float rstd = inv_rms(reduce.sum(ss), a.K, a.eps);
@@ -566,10 +585,13 @@ __global__ void __launch_bounds__(NM_MAXK / NQ_SPAN * 32) k_norm_quant(const Nor
                 if (on[i]) {
                     float x[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)   // without the sign
-                        x[e] = __uint_as_float(__float_as_uint(__fmul_rn(v[8 * i + e], rstd)) ^
-                                               ((neg << (31 - 8 * i - e)) & 0x80000000u));
-                    st_vec<XT, false>(row_of<XT>(a.X, m, a.ldx), at0 + 512 * i, 1, narrow<XT>(x));
+                    for (int e = 0; e < 8; e += 2) f2_to(x + e, f2_mul(f2_of(v + 8 * i + e), make_float2(rstd, rstd), a.nz));
+                    uint4 q = narrow<XT>(x);   // without the signs
+                    q.x ^= (neg << (4 * i)) & 0x80008000u;
+                    q.y ^= (neg << (4 * i + 1)) & 0x80008000u;
+                    q.z ^= (neg << (4 * i + 2)) & 0x80008000u;
+                    q.w ^= (neg << (4 * i + 3)) & 0x80008000u;
+                    st_vec<XT, false>(row_of<XT>(a.X, m, a.ldx), at0 + 512 * i, 1, q);
                 }
         }
         // ---- butterfly, stages in ascending order
@@ -633,14 +655,12 @@ __global__ void __launch_bounds__(NM_MAXK / NQ_SPAN * 32) k_norm_quant(const Nor
             const uint32_t at = BITS == 8 ? col0 + 256 * i : (col0 + 256 * i) / 2;
             // fl(u * inv) is at most LEVELS (1 + 2^-23): adding 1.5 * 2^23 (+ 8 for
             // unsigned nibbles) rounds it to an integer, ties to even, whose bits end
-            // the sum.  The product is rounded on its own (a packed one would be
-            // merged with the sum).
+            // the sum.  The product is rounded on its own.
             constexpr float MAGIC = BITS == 8 ? 12582912.0f : 12582920.0f;
             uint32_t c[8];
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
-                const float2 s = f2_add(make_float2(__fmul_rn(v[8 * i + e], inv), __fmul_rn(v[8 * i + e + 1], inv)),
-                                        make_float2(MAGIC, MAGIC));
+                const float2 s = f2_add(f2_mul(f2_of(v + 8 * i + e), make_float2(inv, inv), a.nz), make_float2(MAGIC, MAGIC));
                 c[e] = __float_as_uint(s.x);
                 c[e + 1] = __float_as_uint(s.y);
             }
@@ -789,6 +809,7 @@ extern "C" hq_status hq_norm_rotate_quant(const void* H, int64_t ld_h, const voi
     a.M = static_cast<int>(M);
     a.K = static_cast<int>(K);
     a.group = group;
+    a.nz = make_float2(-0.0f, -0.0f);
     a.cg = static_cast<float>(1.0 / __builtin_sqrt(static_cast<double>(group)));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (xt == HQ_F16) return bits == 8 ? launch_norm_quant<HQ_F16, 8>(a, st) : launch_norm_quant<HQ_F16, 4>(a, st);
