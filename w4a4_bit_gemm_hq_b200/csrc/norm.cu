@@ -383,10 +383,12 @@ __global__ void __launch_bounds__(MAXT, !KEEP && MAXT == 512 ? 2 : 1) k_residual
 // and back to A for the codes.  Channel c of the row is stored at c + 4 (c / 32) +
 // 8 (c / 256), which makes the accesses of all layouts free of bank conflicts; the
 // weights lie in slots of 16 bytes that only their lane uses.
-// Measured: 2048 x 4096, group 4096, 8 bits 19.5 us (9.0 at HBM's rate), 8192 x 8192,
-// group 256, 4 bits and the normed rows 126 us (87).  Bound by the latency of its
-// instructions at 16 warps per SM (128 registers): about 35 per value, issued at
-// 0.55 per cycle and scheduler; at 80 or 96 registers it spills and is slower.
+// Measured: 2048 x 4096, group 4096, 8 bits 18.7 us (9.0 at HBM's rate); 8192 x 8192,
+// group 256, 4 bits, the normed rows and a gate per channel 116 us (87), per token 126
+// (107).  Bound by the latency of its instructions at 16 warps per SM (128 registers):
+// about 34 per value, issued at 0.5 per cycle and scheduler.  With fewer registers it
+// spills and is slower; with 16 values per thread and 32 warps per SM the work per row
+// and thread (reductions, divisions, addresses) weighs twice: 20.3 and 160 us.
 // A and B stay within the warp; D of groups of 2048 and 4096 needs the CTA.
 __host__ __device__ constexpr int nq_at(int c) { return c + 4 * (c >> 5) + 8 * (c >> 8); }
 constexpr int NQ_SPAN = 1024;                 // channels of a warp
@@ -472,9 +474,13 @@ __device__ __forceinline__ void stages_d(float (&v)[32], float* base, int t) {
         for (int j = 0; j < J; ++j) p[nq_at(8 * J * q) + nq_at(256) * j] = v[q * J + j];
 }
 
-// FULL: rows of a multiple of 1024 channels, every vector is there
-template <int XT, int BITS, bool FULL>
-__global__ void __launch_bounds__(NM_MAXK / NQ_SPAN * 32) k_norm_quant(const NormArgs a) {
+// FULL: rows of a multiple of 1024 channels, every vector is there.
+// IN: the operands beside H: none, Y, or Y and the gate, whose next row is requested
+// before the codes are written (at its use it cost 180 us in place of 126 at 8192 x
+// 8192).  Without Y the registers allow 20 warps per SM (8192 x 4096, group 128: 35.4 us,
+// 37.8 at 16; rows of more than 10 warps do not gain).
+template <int XT, int BITS, bool FULL, int IN>
+__global__ void __launch_bounds__(IN == 0 ? 640 : 512) k_norm_quant(const NormArgs a) {
     __shared__ float2 red[2][32];
     extern __shared__ __align__(16) float dyn[];   // weights, then the row
     // the small-M GEMM may be launched early: it waits for this grid's
@@ -500,13 +506,19 @@ __global__ void __launch_bounds__(NM_MAXK / NQ_SPAN * 32) k_norm_quant(const Nor
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             q.h[i] = ld_vec<XT, false>(row_of<XT>(a.H, m, a.ldh), at0 + 512 * i, on[i]);
-        if (a.Y != nullptr) {
+        if constexpr (IN > 0) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 q.y[i] = ld_vec<XT, false>(row_of<XT>(a.Y, m, a.ldy), at0 + 512 * i, on[i]);
         }
     };
     load(blockIdx.x, r);
+    uint4 gv[4];
+    if constexpr (IN > 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            gv[i] = ld_vec<XT, false>(row_of<XT>(a.gate, blockIdx.x, a.ldg), at0 + 512 * i, on[i]);
+    }
     // weights of this lane's channels (each lane reads back what it wrote), and the
     // signs of d: those of pair 4 i + e / 2 in bits 15 and 31 less the pair's number
     uint32_t neg = 0;
@@ -546,12 +558,12 @@ __global__ void __launch_bounds__(NM_MAXK / NQ_SPAN * 32) k_norm_quant(const Nor
         for (int i = 0; i < 4; ++i) {
             float h[8];
             widen<XT>(r.h[i], h);
-            if (a.Y != nullptr) {
+            if constexpr (IN > 0) {
                 float p[8];
                 widen<XT>(r.y[i], p);
-                if (a.gate != nullptr && on[i]) {
+                if constexpr (IN > 1) {
                     float g[8];
-                    widen<XT>(ld_vec<XT, false>(row_of<XT>(a.gate, m, a.ldg), at0 + 512 * i, 1), g);
+                    widen<XT>(gv[i], g);
 #pragma unroll
                     for (int e = 0; e < 8; e += 2) f2_to(p + e, f2_mul(f2_of(g + e), f2_of(p + e), a.nz));
                 }
@@ -646,6 +658,13 @@ __global__ void __launch_bounds__(NM_MAXK / NQ_SPAN * 32) k_norm_quant(const Nor
                     v[8 * i + e] = f.x; v[8 * i + e + 1] = f.y; v[8 * i + e + 2] = f.z; v[8 * i + e + 3] = f.w;
                 }
         }
+        if (m + gridDim.x < a.M) {
+        if constexpr (IN > 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                gv[i] = ld_vec<XT, false>(row_of<XT>(a.gate, m + gridDim.x, a.ldg), at0 + 512 * i, on[i]);
+        }
+        }
         constexpr float LEVELS = BITS == 8 ? 127.0f : 7.0f;
         const float inv = t.y == 0.f ? 0.f : __fdiv_rn(LEVELS, t.y);
 #pragma unroll
@@ -733,9 +752,14 @@ hq_status launch_norm_quant(const NormArgs& a, cudaStream_t st) {
     const int warps = (a.K + NQ_SPAN - 1) / NQ_SPAN;
     const int smem = warps * (NQ_BUF + NQ_SPAN) * static_cast<int>(sizeof(float));
     const bool full = a.K % NQ_SPAN == 0;
-    auto kern = full ? k_norm_quant<XT, BITS, true> : k_norm_quant<XT, BITS, false>;
-    static SmemOptIn opt_in[2];
-    if (!allow_smem(opt_in[full], kern, smem)) return HQ_ERR_CUDA;
+    const int in = a.Y == nullptr ? 0 : a.gate == nullptr ? 1 : 2;
+    auto pick = [&](auto f) {
+        constexpr bool F = decltype(f)::value;
+        return in == 0 ? k_norm_quant<XT, BITS, F, 0> : in == 1 ? k_norm_quant<XT, BITS, F, 1> : k_norm_quant<XT, BITS, F, 2>;
+    };
+    auto kern = full ? pick(std::true_type{}) : pick(std::false_type{});
+    static SmemOptIn opt_in[6];
+    if (!allow_smem(opt_in[(full ? 3 : 0) + in], kern, smem)) return HQ_ERR_CUDA;
     const unsigned grid = grid_for(kern, 32 * warps, smem, a.M);
     if (grid == 0) return HQ_ERR_CUDA;
     kern<<<grid, 32 * warps, smem, st>>>(a);
