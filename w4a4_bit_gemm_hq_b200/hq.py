@@ -370,16 +370,16 @@ def _device(t, name):
     return dev
 
 
-def _rows(t, name, dev, M, K, dtype):
-    """Row stride in elements of an [M, K] tensor whose rows are contiguous."""
-    if t.get_device() != dev or t.dtype is not dtype or t.shape != (M, K):
-        raise ValueError("%s must be a %s tensor of shape (%d, %d) on the device of the first argument"
-                         % (name, dtype, M, K))
+def _rows(t, name, dev, shape, dtype):
+    """Row stride in elements of a matrix of `shape` whose rows are contiguous."""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
+        raise ValueError("%s must be a %s tensor of shape %s on the device of the first argument"
+                         % (name, dtype, tuple(shape)))
     s0, s1 = t.stride()
-    if s1 != 1 and K > 1 and M > 0:
+    if s1 != 1 and shape[1] > 1 and shape[0] > 0:
         raise ValueError("%s must have contiguous rows" % name)
     # the stride of a single row (or of none) says nothing
-    return s0 if M > 1 else max(K + 7 & ~7, s0 & ~7)
+    return s0 if shape[0] > 1 else max(shape[1] + 7 & ~7, s0 & ~7)
 
 
 def _whole(t, name, dev, shape, dtype):
@@ -388,8 +388,8 @@ def _whole(t, name, dev, shape, dtype):
                          % (name, dtype, tuple(shape)))
 
 
-def _launch(dev, fn, where, *args):
-    if torch.cuda.current_device() == dev:
+def _launch(dev, fn, where, args):
+    if torch._C._cuda_getDevice() == dev:
         status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
@@ -398,27 +398,12 @@ def _launch(dev, fn, where, *args):
         raise HQError(status, where)
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
-def _norm_args(H, dev, w, Y, w_post, gate, H_out, X, M, K):
-    """Checks shared by the two calls below; the row strides (H, Y, gate, H_out, X) and the weights' type."""
-    dt = H.dtype
-    wt = w.dtype if w is not None else w_post.dtype if w_post is not None else dt
-    if w is not None:
-        _whole(w, "w", dev, (K,), wt)
-    if w_post is not None:
-        _whole(w_post, "w_post", dev, (K,), wt)
-    ld_g = 0
-    if gate is not None:
-        if gate.dim() == 1:
-            _whole(gate, "gate", dev, (K,), dt)
-        else:
-            ld_g = _rows(gate, "gate", dev, M, K, dt)
-    return (_rows(H, "H", dev, M, K, dt), 0 if Y is None else _rows(Y, "Y", dev, M, K, dt), ld_g,
-            0 if H_out is None else _rows(H_out, "H_out", dev, M, K, dt),
-            0 if X is None else _rows(X, "X", dev, M, K, dt), dtype_code(wt))
+def _gate_args(gate, dev, shape, dtype):
+    """(address, row stride) of the gate: one row [K] for all (stride 0) or [M, K]."""
+    if gate.dim() == 1:
+        _whole(gate, "gate", dev, shape[1:], dtype)
+        return gate.data_ptr(), 0
+    return gate.data_ptr(), _rows(gate, "gate", dev, shape, dtype)
 
 
 def _new_rows(like, M, K):
@@ -435,14 +420,35 @@ def hq_residual_norm(H, w, eps, Y=None, w_post=None, gate=None, alpha=1.0, w_off
     None).  gate is [K] or [M, K]; w_offset is added to w and w_post.  H_out may
     be H (in place) and X may be Y; without Y there is no H_out unless one is given."""
     dev = _device(H, "H")
-    M, K = H.shape
-    if Y is not None and H_out is None:
-        H_out = _new_rows(H, M, K)
-    if w is not None and X is None:
-        X = _new_rows(H, M, K)
-    ld_h, ld_y, ld_g, ld_ho, ld_x, wt = _norm_args(H, dev, w, Y, w_post, gate, H_out, X, M, K)
-    _launch(dev, lib.hq_residual_norm, "hq_residual_norm", H.data_ptr(), ld_h, _at(Y), ld_y, dtype_code(H.dtype), M, K,
-            _at(w_post), _at(gate), ld_g, alpha, _at(w), wt, w_offset, eps, _at(H_out), ld_ho, _at(X), ld_x)
+    dt, shape = H.dtype, H.shape
+    M, K = shape
+    wt = dt
+    p_y = p_post = p_gate = p_w = p_ho = p_x = None
+    ld_h = _rows(H, "H", dev, shape, dt)
+    ld_y = ld_g = ld_ho = ld_x = 0
+    if Y is not None:
+        ld_y, p_y = _rows(Y, "Y", dev, shape, dt), Y.data_ptr()
+        if H_out is None:
+            H_out = _new_rows(H, M, K)
+    if w is not None:
+        wt = w.dtype
+        _whole(w, "w", dev, (K,), wt)
+        p_w = w.data_ptr()
+        if X is None:
+            X = _new_rows(H, M, K)
+    if w_post is not None:
+        wt = w_post.dtype if w is None else wt
+        _whole(w_post, "w_post", dev, (K,), wt)
+        p_post = w_post.data_ptr()
+    if gate is not None:
+        p_gate, ld_g = _gate_args(gate, dev, shape, dt)
+    if H_out is not None:
+        ld_ho, p_ho = _rows(H_out, "H_out", dev, shape, dt), H_out.data_ptr()
+    if X is not None:
+        ld_x, p_x = _rows(X, "X", dev, shape, dt), X.data_ptr()
+    _launch(dev, lib.hq_residual_norm, "hq_residual_norm",
+            (H.data_ptr(), ld_h, p_y, ld_y, dtype_code(dt), M, K, p_post, p_gate, ld_g, alpha, p_w, dtype_code(wt),
+             w_offset, eps, p_ho, ld_ho, p_x, ld_x))
     return H_out, X
 
 
@@ -452,26 +458,43 @@ def hq_norm_rotate_quant(H, w, eps, group, H_signs=None, Y=None, gate=None, alph
     hq_rotate_quant (bits=4) or hq_rotate_quant8 (bits=8) in one pass; the
     normed rows X only with want_x or an X to write."""
     dev = _device(H, "H")
-    M, K = H.shape
-    if Y is not None and H_out is None:
-        H_out = _new_rows(H, M, K)
-    if want_x and X is None:
+    dt, shape = H.dtype, H.shape
+    M, K = shape
+    wt = dt
+    p_w = p_y = p_gate = p_ho = p_x = p_d = None
+    ld_h = _rows(H, "H", dev, shape, dt)
+    ld_y = ld_g = ld_ho = ld_x = 0
+    if w is not None:
+        wt = w.dtype
+        _whole(w, "w", dev, (K,), wt)
+        p_w = w.data_ptr()
+    if Y is not None:
+        ld_y, p_y = _rows(Y, "Y", dev, shape, dt), Y.data_ptr()
+        if H_out is None:
+            H_out = _new_rows(H, M, K)
+    if gate is not None:
+        p_gate, ld_g = _gate_args(gate, dev, shape, dt)
+    if H_out is not None:
+        ld_ho, p_ho = _rows(H_out, "H_out", dev, shape, dt), H_out.data_ptr()
+    if X is None and want_x:
         X = _new_rows(H, M, K)
-    shape, dtype = ((M, K), torch.int8) if bits == 8 else ((M, K // 2), torch.uint8)
+    if X is not None:
+        ld_x, p_x = _rows(X, "X", dev, shape, dt), X.data_ptr()
+    if H_signs is not None:
+        _whole(H_signs, "H_signs", dev, (group,), torch.int8)
+        p_d = H_signs.data_ptr()
+    codes, ct = ((M, K), torch.int8) if bits == 8 else ((M, K // 2), torch.uint8)
     if Xq is None:
-        Xq = torch.empty(shape, dtype=dtype, device=H.device)
+        Xq = torch.empty(codes, dtype=ct, device=H.device)
     else:
-        _whole(Xq, "Xq", dev, shape, dtype)
+        _whole(Xq, "Xq", dev, codes, ct)
     if sx is None:
         sx = torch.empty((M,), dtype=torch.float32, device=H.device)
     else:
         _whole(sx, "sx", dev, (M,), torch.float32)
-    if H_signs is not None:
-        _whole(H_signs, "H_signs", dev, (group,), torch.int8)
-    ld_h, ld_y, ld_g, ld_ho, ld_x, wt = _norm_args(H, dev, w, Y, None, gate, H_out, X, M, K)
-    _launch(dev, lib.hq_norm_rotate_quant, "hq_norm_rotate_quant", H.data_ptr(), ld_h, _at(Y), ld_y,
-            dtype_code(H.dtype), M, K, _at(gate), ld_g, alpha, _at(w), wt, w_offset, eps, group, _at(H_signs), bits,
-            _at(H_out), ld_ho, _at(X), ld_x, Xq.data_ptr(), sx.data_ptr())
+    _launch(dev, lib.hq_norm_rotate_quant, "hq_norm_rotate_quant",
+            (H.data_ptr(), ld_h, p_y, ld_y, dtype_code(dt), M, K, p_gate, ld_g, alpha, p_w, dtype_code(wt),
+             w_offset, eps, group, p_d, bits, p_ho, ld_ho, p_x, ld_x, Xq.data_ptr(), sx.data_ptr()))
     return Xq, sx, H_out, X
 
 
@@ -484,18 +507,19 @@ def hq_lora_plan(ids, n, order=None, tiles=None):
     batch grouped by their adapter ids int32 [M] in [0, n), -1 for none.  One
     plan serves every adapted layer of the step."""
     dev = _device(ids, "ids")
-    M = ids.shape[0]
+    shape = ids.shape
+    M = shape[0]
     _whole(ids, "ids", dev, (M,), torch.int32)
     rows = hq_lora_max_tiles(M, n)
     if order is None:
         order = torch.empty((M,), dtype=torch.int32, device=ids.device)
     else:
-        _whole(order, "order", dev, (M,), torch.int32)
+        _whole(order, "order", dev, shape, torch.int32)
     if tiles is None:
         tiles = torch.empty((rows, 3), dtype=torch.int32, device=ids.device)
     else:
         _whole(tiles, "tiles", dev, (rows, 3), torch.int32)
-    _launch(dev, lib.hq_lora_plan, "hq_lora_plan", ids.data_ptr(), M, n, order.data_ptr(), tiles.data_ptr())
+    _launch(dev, lib.hq_lora_plan, "hq_lora_plan", (ids.data_ptr(), M, n, order.data_ptr(), tiles.data_ptr()))
     return order, tiles
 
 
@@ -509,31 +533,38 @@ def hq_lora_apply(X, A, B, order, tiles, ranks=None, scales=None, base=None, Y=N
     [n, N, r_max] have X's type; order and tiles come from hq_lora_plan.  Y may be
     base (in place); it has base's type, or out_dtype (X's by default)."""
     dev = _device(X, "X")
-    dt = X.dtype
-    M, K = X.shape
+    dt, shape = X.dtype, X.shape
+    M, K = shape
     n, r, _ = A.shape
     N = B.shape[1]
     if Y is None:
         yt = base.dtype if base is not None else dt if out_dtype is None else out_dtype
         Y = torch.empty((M, N), dtype=yt, device=X.device)
     yt = Y.dtype
-    ld_x, ld_y = _rows(X, "X", dev, M, K, dt), _rows(Y, "Y", dev, M, N, yt)
-    ld_b = 0 if base is None else ld_y if base is Y else _rows(base, "base", dev, M, N, yt)
+    out = (M, N)
+    ld_x, ld_y = _rows(X, "X", dev, shape, dt), _rows(Y, "Y", dev, out, yt)
+    p_base = p_ranks = p_scales = None
+    ld_b = 0
+    if base is not None:
+        ld_b, p_base = ld_y if base is Y else _rows(base, "base", dev, out, yt), base.data_ptr()
     _whole(A, "A", dev, (n, r, K), dt)
     _whole(B, "B", dev, (n, N, r), dt)
     _whole(order, "order", dev, (M,), torch.int32)
     _whole(tiles, "tiles", dev, (hq_lora_max_tiles(M, n), 3), torch.int32)
     if ranks is not None:
         _whole(ranks, "ranks", dev, (n,), torch.int32)
+        p_ranks = ranks.data_ptr()
     if scales is not None:
         _whole(scales, "scales", dev, (n,), torch.float32)
+        p_scales = scales.data_ptr()
     if workspace is None:
         workspace = torch.empty((M, r), dtype=torch.float32, device=X.device)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the device of X")
-    _launch(dev, lib.hq_lora_apply, "hq_lora_apply", X.data_ptr(), dtype_code(dt), M, K, ld_x, A.data_ptr(),
-            B.data_ptr(), N, n, r, _at(ranks), _at(scales), order.data_ptr(), tiles.data_ptr(), _at(base), ld_b,
-            Y.data_ptr(), dtype_code(yt), ld_y, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _launch(dev, lib.hq_lora_apply, "hq_lora_apply",
+            (X.data_ptr(), dtype_code(dt), M, K, ld_x, A.data_ptr(), B.data_ptr(), N, n, r, p_ranks, p_scales,
+             order.data_ptr(), tiles.data_ptr(), p_base, ld_b, Y.data_ptr(), dtype_code(yt), ld_y,
+             workspace.data_ptr(), workspace.numel() * workspace.element_size()))
     return Y
 
 
