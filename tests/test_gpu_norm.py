@@ -288,6 +288,22 @@ def test_norm_rotate_quant(M, K, group, bits, xt, wt, block, gate, alpha, off, s
     assert (np.abs(unpack(Xq, bits) * step - u) <= tol).all()
 
 
+@pytest.mark.parametrize("gate", ["channel", "token"])
+@pytest.mark.parametrize("M,K,group,bits", [(1500, 4096, 256, 4), (700, 8192, 4096, 8)])
+def test_quantiser_in_place_over_several_rows_per_cta(M, K, group, bits, gate):
+    """The operands of a CTA's next row are read before this row is finished: the rows
+    of the block and of the stream that it overwrites are other ones."""
+    H, Y, w, _, g = inputs(M, K, BF16, BF16, False, gate, 0)
+    want = hq.hq_norm_rotate_quant(H, w, 1e-5, group, Y=Y, gate=g, alpha=0.5, bits=bits, want_x=True)
+    want_h, want_q, amax = codes_fp32(H, Y, g, 0.5, w, 0.0, group, None, bits)
+    assert np.array_equal(f32(want[2]), want_h) and np.array_equal(unpack(want[0], bits), want_q)
+    check_scale(want[1], want_h, w, 0.0, 1e-5, group, amax, bits)
+    check_normed(want[3], want[2], w, 0.0, 1e-5)
+    got = hq.hq_norm_rotate_quant(H, w, 1e-5, group, Y=Y, gate=g, alpha=0.5, bits=bits, H_out=H, X=Y)
+    assert got[2] is H and got[3] is Y
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_quantiser_rows_of_zeros_nan_and_infinity():
     M, K = 6, 2048
     H, w = rows(M, K, BF16, 3), weights(K, BF16, 4)
