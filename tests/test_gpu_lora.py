@@ -177,6 +177,18 @@ def test_apply(M, K, N, n, r, xt, yt, ragged, runs):
     assert torch.equal(apply(d, Y=d["base"]), Y) and torch.equal(d["base"], Y)   # in place
 
 
+@pytest.mark.parametrize("M,K,N,n,r,xt,yt,ragged,runs", [
+    (2100, 96, 1320, 3, 24, F16, F32, True, 150),
+    (2100, 96, 1320, 3, 24, BF16, F32, False, 150),
+    (2100, 128, 1320, 3, 72, BF16, BF16, False, 150),
+    (2500, 64, 2056, 2, 200, F16, F16, True, 1),
+    (2100, 64, 1320, 3, 192, BF16, F32, False, 90),
+])
+def test_apply_with_ctas_for_the_whole_gpu(M, K, N, n, r, xt, yt, ragged, runs):
+    """Two CTAs per SM with fewer base rows asked for ahead, or one round of larger CTAs."""
+    test_apply(M, K, N, n, r, xt, yt, ragged, runs)
+
+
 @pytest.mark.parametrize("M,runs", [(130, 13), (5, 1)])
 @pytest.mark.parametrize("yt", [F16, BF16, F32])
 def test_no_base_no_ranks_no_scales(yt, M, runs):

@@ -745,6 +745,7 @@ __global__ void __launch_bounds__(few_threads<RC>) k_lora_few(const ShrinkArgs s
 constexpr int EX_THREADS = 256;                 // those that copy and store
 constexpr int EX_ROWS = 2 * LR_TILE;            // tokens of a product
 constexpr int EX_NB = 64;                       // columns of a block
+constexpr int kTwoDynSmem = 228 * 1024 / 2 - 1024 - 256;   // for two CTAs on an SM, beside the static part
 
 __host__ __device__ constexpr int ex_terms(bool bf, int yt) { return bf && yt == HQ_F32 ? 3 : 2; }
 // bytes of shared memory: t, two blocks of B, base (`depth` blocks), row scales
@@ -1149,7 +1150,32 @@ hq_status launch_expand(ExpandArgs a, int tiles, cudaStream_t st) {
         cfg.blockDim = dim3(FEW_THREADS);
         return cudaLaunchKernelEx(&cfg, k_lora_expand_few<BF, YT>, a) == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
     }
-    for (a.depth = 3; a.depth > 1 && ex_smem(BF, YT, atoms, a.depth) > kMaxDynSmem; --a.depth) {}
+    // a CTA stages its tiles' t once for all its blocks of columns: as many CTAs as
+    // the GPU holds at once (two per SM), counting at most `heads` tiles that lead
+    // a pair; three rounds of smaller CTAs measured 2% (8192 x 28672) to 15%
+    // (2048 x 4096) slower
+    const int64_t nblk = (a.N + EX_NB - 1) / EX_NB;
+    const int heads = (tiles + (a.n < tiles ? a.n : tiles) + 1) / 2;
+    auto strips_for = [&](int per_sm) {
+        const int64_t s = 148 * per_sm / heads;
+        return s < 1 ? 1 : s > nblk ? nblk : s;
+    };
+    int64_t strips = strips_for(2);
+    a.depth = 3;
+    // Where every SM is sure to have a CTA, two of them per SM are worth more than blocks
+    // asked for ahead (fp32 Y, 8192 x 4096 -> 11008, rank 32: 236 us in place of 247), and
+    // where shared memory has room for one only (ranks above 64), one round of larger
+    // CTAs more than two of smaller ones (2048 x 4096 -> 4096, rank 128: 44.8 us, 48.5; 8192
+    // x 4096 -> 11008, rank 256: 207, 219).  With fewer CTAs it is the other way round (442
+    // tokens of one adapter, 184 -> 3864, fp32 Y: 16 us, 22 to 24).
+    if ((static_cast<int64_t>(a.M) + EX_ROWS - 1) / EX_ROWS * strips >= 148) {
+        while (a.depth > 1 && ex_smem(BF, YT, atoms, a.depth) > kTwoDynSmem) --a.depth;
+        if (ex_smem(BF, YT, atoms, a.depth) > kTwoDynSmem) {
+            a.depth = 3;
+            strips = strips_for(1);
+        }
+    }
+    while (a.depth > 1 && ex_smem(BF, YT, atoms, a.depth) > kMaxDynSmem) --a.depth;
     const int smem = ex_smem(BF, YT, atoms, a.depth);
     const int rk = a.r <= 16 ? 0 : a.r <= 32 ? 1 : a.r <= 64 ? 2 : 3;
     auto kern = rk == 0   ? k_lora_expand<BF, YT, 16>
@@ -1158,14 +1184,6 @@ hq_status launch_expand(ExpandArgs a, int tiles, cudaStream_t st) {
                           : k_lora_expand<BF, YT, 256>;
     static SmemOptIn opt_in[4];
     if (!allow_smem(opt_in[rk], kern, smem)) return HQ_ERR_CUDA;
-    // a CTA stages its tiles' t once for all its blocks of columns: as many CTAs as
-    // the GPU holds at once (two per SM), counting at most `heads` tiles that lead
-    // a pair; three rounds of smaller CTAs measured 2% (8192 x 28672) to 15%
-    // (2048 x 4096) slower
-    const int64_t nblk = (a.N + EX_NB - 1) / EX_NB;
-    const int heads = (tiles + (a.n < tiles ? a.n : tiles) + 1) / 2;
-    int64_t strips = 148 * 2 / heads;
-    strips = strips < 1 ? 1 : strips > nblk ? nblk : strips;
     const int64_t per = (nblk + strips - 1) / strips;
     a.blocks = static_cast<int>(per);
     a.ntiles = tiles;
