@@ -417,6 +417,7 @@ struct ExpandArgs {
     void* Y;
     int64_t ldb, ldy;
     int M, N, n, r, ntiles;
+    bool wide;           // k_lora_expand: rows of an fp32 Y start on 32-byte boundaries
     int blocks, depth;   // k_lora_expand: column blocks of a CTA, blocks of base rows in shared memory
 };
 
@@ -1064,6 +1065,7 @@ __global__ void __launch_bounds__(EX_THREADS + 32, 2) k_lora_expand(const Expand
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if (CHECK && (m[f][h] < 0 || left <= 0)) continue;
+                        uint32_t both[PIECES][4];
 #pragma unroll
                         for (int e = 0; e < PIECES; ++e) {
                             uint4 y = make_uint4(0u, 0u, 0u, 0u);
@@ -1085,7 +1087,19 @@ __global__ void __launch_bounds__(EX_THREADS + 32, 2) k_lora_expand(const Expand
                                                     add16<YT == HQ_BF16>(w[k], true, v1));
                                 }
                             }
-                            reinterpret_cast<uint4*>(ydst[f][h] + dbytes)[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                            if (PIECES == 1 || !p.wide)
+                                reinterpret_cast<uint4*>(ydst[f][h] + dbytes)[e] = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) both[e][k] = w[k];
+                        }
+                        if constexpr (PIECES == 2) {
+                            // the halves of a sector one by one took 12% longer (8192 x 11008)
+                            if (p.wide)
+                                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                                                 ydst[f][h] + dbytes),
+                                             "r"(both[0][0]), "r"(both[0][1]), "r"(both[0][2]), "r"(both[0][3]),
+                                             "r"(both[1][0]), "r"(both[1][1]), "r"(both[1][2]), "r"(both[1][3])
+                                             : "memory");
                         }
                     }
             };
@@ -1161,6 +1175,7 @@ hq_status launch_expand(ExpandArgs a, int tiles, cudaStream_t st) {
         return s < 1 ? 1 : s > nblk ? nblk : s;
     };
     int64_t strips = strips_for(2);
+    a.wide = YT == HQ_F32 && (reinterpret_cast<uintptr_t>(a.Y) & 31u) == 0 && a.ldy % 8 == 0;
     a.depth = 3;
     // Where every SM is sure to have a CTA, two of them per SM are worth more than blocks
     // asked for ahead (fp32 Y, 8192 x 4096 -> 11008, rank 32: 236 us in place of 247), and
