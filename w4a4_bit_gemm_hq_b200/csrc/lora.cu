@@ -735,7 +735,7 @@ __global__ void __launch_bounds__(few_threads<RC>) k_lora_few(const ShrinkArgs s
 //    2 t + e of each 32 the output column 8 t + 2 i + e: a lane of the
 //    16x256b accumulator layout then holds 8 consecutive outputs of a row.
 //  * the next two blocks' B and the next `depth` blocks' base rows (in slots
-//    that only their lane uses) are on their way (cp.async) while a block is
+//    that only their warp uses) are on their way (cp.async) while a block is
 //    multiplied and stored; two CTAs per SM cover each other's waits.
 // Two neighbouring tiles of one adapter are taken together.  What bounds it now is
 // the latency of a block's chain (copies awaited, barrier, accumulators read, four
@@ -946,6 +946,14 @@ __global__ void __launch_bounds__(EX_THREADS + 32, 2) k_lora_expand(const Expand
     int64_t ybytes = 0;                              // from the first block on
     // a warp whose rows are all there, with a base: no checks but for the last block
     const bool whole = __all_sync(0xFFFFFFFFu, p.base != nullptr && m[0][0] >= 0 && m[0][1] >= 0 && m[1][0] >= 0 && m[1][1] >= 0);
+    // Chunk j (16 bytes) of the 8 that four lanes share of an fp32 row is asked for by
+    // lane (j ^ j / 4) % 4, so that each of its two copies takes whole sectors with
+    // its neighbours', and each of its reads has a bank of its own.  ahead(e): where
+    // copy e lies, in chunks from this lane's first column
+    auto ahead = [&](int e) { return PIECES == 1 ? 0 : 4 * e + (t4 ^ e) - 2 * t4; };
+    auto base_slot = [&](int e) {   // of this lane's chunk e
+        return PIECES == 1 ? 0 : (t4 >> 1) * EX_THREADS * 16 + 16 * ((((2 * t4 + e) & 3) ^ (t4 >> 1)) - t4);
+    };
     auto load_base = [&](bool more, int slot) {
         if (!more) return;
         const uint32_t sd = slot0 + slot * BASE;
@@ -954,10 +962,11 @@ __global__ void __launch_bounds__(EX_THREADS + 32, 2) k_lora_expand(const Expand
         for (int f = 0; f < 2; ++f)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                if (all || (ysrc[f][h] != nullptr && yleft > 0)) {
+                if (all || ysrc[f][h] != nullptr) {
 #pragma unroll
                     for (int e = 0; e < PIECES; ++e)
-                        cp_async16(sd + ((f * 2 + h) * PIECES + e) * EX_THREADS * 16, ysrc[f][h] + ybytes + 16 * e);
+                        if (all || yleft > (16 / ES) * ahead(e))
+                            cp_async16(sd + ((f * 2 + h) * PIECES + e) * EX_THREADS * 16, ysrc[f][h] + ybytes + 16 * ahead(e));
                 }
             }
         ybytes += EX_NB * ES;
@@ -1070,7 +1079,7 @@ __global__ void __launch_bounds__(EX_THREADS + 32, 2) k_lora_expand(const Expand
                         for (int e = 0; e < PIECES; ++e) {
                             uint4 y = make_uint4(0u, 0u, 0u, 0u);
                             if (!CHECK || p.base != nullptr)
-                                y = *reinterpret_cast<const uint4*>(sd + ((f * 2 + h) * PIECES + e) * EX_THREADS * 16);
+                                y = *reinterpret_cast<const uint4*>(sd + (f * 2 + h) * PIECES * EX_THREADS * 16 + base_slot(e));
                             uint32_t w[4] = {y.x, y.y, y.z, y.w};
                             constexpr int PER = YT == HQ_F32 ? 1 : 2;   // outputs per word
 #pragma unroll
@@ -1107,6 +1116,7 @@ __global__ void __launch_bounds__(EX_THREADS + 32, 2) k_lora_expand(const Expand
                 store(std::false_type{});
             else
                 store(std::true_type{});
+            if constexpr (PIECES == 2) __syncwarp();   // the slots are the warp's
             load_base(blk + p.depth < blk1, slot);
         }
         cp_async_commit();
