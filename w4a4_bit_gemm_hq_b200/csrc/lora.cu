@@ -948,7 +948,8 @@ __global__ void __launch_bounds__(EX_THREADS + 32, 2) k_lora_expand(const Expand
     const bool whole = __all_sync(0xFFFFFFFFu, p.base != nullptr && m[0][0] >= 0 && m[0][1] >= 0 && m[1][0] >= 0 && m[1][1] >= 0);
     // Chunk j (16 bytes) of the 8 that four lanes share of an fp32 row is asked for by
     // lane (j ^ j / 4) % 4, so that each of its two copies takes whole sectors with
-    // its neighbours', and each of its reads has a bank of its own.  ahead(e): where
+    // its neighbours' (half sectors took 27% longer at 8192 x 11008, rank 32), and its reads
+    // have no bank conflicts.  ahead(e): where
     // copy e lies, in chunks from this lane's first column
     auto ahead = [&](int e) { return PIECES == 1 ? 0 : 4 * e + (t4 ^ e) - 2 * t4; };
     auto base_slot = [&](int e) {   // of this lane's chunk e
@@ -1102,7 +1103,7 @@ __global__ void __launch_bounds__(EX_THREADS + 32, 2) k_lora_expand(const Expand
                             for (int k = 0; k < 4; ++k) both[e][k] = w[k];
                         }
                         if constexpr (PIECES == 2) {
-                            // the halves of a sector one by one took 12% longer (8192 x 11008)
+                            // the halves of a sector one by one took 12% longer (8192 x 11008, rank 32)
                             if (p.wide)
                                 asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
                                                  ydst[f][h] + dbytes),
@@ -1188,11 +1189,12 @@ hq_status launch_expand(ExpandArgs a, int tiles, cudaStream_t st) {
     a.wide = YT == HQ_F32 && (reinterpret_cast<uintptr_t>(a.Y) & 31u) == 0 && a.ldy % 8 == 0;
     a.depth = 3;
     // Where every SM is sure to have a CTA, two of them per SM are worth more than blocks
-    // asked for ahead (fp32 Y, 8192 x 4096 -> 11008, rank 32: 236 us in place of 247), and
-    // where shared memory has room for one only (ranks above 64), one round of larger
-    // CTAs more than two of smaller ones (2048 x 4096 -> 4096, rank 128: 44.8 us, 48.5; 8192
-    // x 4096 -> 11008, rank 256: 207, 219).  With fewer CTAs it is the other way round (442
-    // tokens of one adapter, 184 -> 3864, fp32 Y: 16 us, 22 to 24).
+    // asked for ahead (fp32 Y, 8192 x 4096 -> 11008, rank 32: fp16 173 us in place of 185,
+    // bf16 166 and 162; 2024 x 168 -> 1320: 17.1, 19.2), and where shared memory has room
+    // for one only (ranks above 64), one round of larger CTAs more than two of smaller ones
+    // (2048 x 4096 -> 4096, rank 128: 45 us, 48.7; 8192 x 4096 -> 11008, rank 256: 207,
+    // 219).  With fewer CTAs it is the other way round (442 tokens of one adapter, 184 ->
+    // 3864, fp32 Y: 22 in place of 16 us when it was tried, 14 now).
     if ((static_cast<int64_t>(a.M) + EX_ROWS - 1) / EX_ROWS * strips >= 148) {
         while (a.depth > 1 && ex_smem(BF, YT, atoms, a.depth) > kTwoDynSmem) --a.depth;
         if (ex_smem(BF, YT, atoms, a.depth) > kTwoDynSmem) {
