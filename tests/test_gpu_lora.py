@@ -189,6 +189,21 @@ def test_apply_with_ctas_for_the_whole_gpu(M, K, N, n, r, xt, yt, ragged, runs):
     test_apply(M, K, N, n, r, xt, yt, ragged, runs)
 
 
+@pytest.mark.parametrize("xt", [F16, BF16])
+def test_fp32_rows_between_sectors(xt):
+    """Rows of Y and base that start on 16-byte boundaries only, and columns that end inside a block."""
+    M, N = 700, 328
+    d = batch(M, 128, N, 2, 24, xt, F32, seed=9, ragged=True, runs=100)
+    want = apply(d)
+    check(want, d)
+    base = torch.full((M, N + 4), 7.0, device="cuda")
+    base[:, :N] = d["base"]
+    Y = torch.full((M, N + 12), 7.0, device="cuda")
+    assert torch.equal(apply(d, base=base[:, :N], Y=Y[:, 4:N + 4]), want)
+    assert (Y[:, :4] == 7).all() and (Y[:, N + 4:] == 7).all()
+    assert torch.equal(apply(d, base=base[:, :N], Y=base[:, :N]), want) and (base[:, N:] == 7).all()
+
+
 @pytest.mark.parametrize("M,runs", [(130, 13), (5, 1)])
 @pytest.mark.parametrize("yt", [F16, BF16, F32])
 def test_no_base_no_ranks_no_scales(yt, M, runs):
