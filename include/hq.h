@@ -569,7 +569,8 @@ hq_status hq_residual_norm(const void* H, int64_t ld_h, const void* Y, int64_t l
  *           NULL (X: the normed rows, for callers that need them as well)
  *  group, H_signs   as hq_rotate_quant
  *  bits     4: Xq device, [M][K/2] packed codes; 8: [M][K] int8 codes (output)
- *  sx       device, [M] fp32 (output); NaN for a row that holds a NaN or infinity
+ *  sx       device, [M] fp32 (output); NaN for a row with a NaN or infinity in h, in the
+ *           weights or behind the rotation (its codes then say nothing)
  * Errors: as hq_residual_norm and hq_rotate_quant; HQ_ERR_ARG for other bits.
  */
 hq_status hq_norm_rotate_quant(const void* H, int64_t ld_h, const void* Y, int64_t ld_y, hq_dtype xt, int64_t M,

@@ -189,7 +189,7 @@ struct RowReduce {
         for (int o = 16; o > 0; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, s, o));
         return s;
     }
-    // a is not negative: its bits are ordered as it is
+    // a is not negative: its bits are ordered as it is, a NaN above infinity
     __device__ __forceinline__ static float lanes_max(float a) {
         return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(a)));
     }
@@ -427,9 +427,11 @@ __device__ __forceinline__ void f2_to(float* v, float2 a) {
     v[0] = a.x;
     v[1] = a.y;
 }
+// NaN if one of them is: infinities that meet in the butterfly leave NaN, and a row
+// of them must not pass for one of small values
 __device__ __forceinline__ float max3_abs(float a, float b, float c) {
     float r;
-    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 
@@ -647,7 +649,7 @@ __global__ void __launch_bounds__(IN == 0 ? 640 : 512) k_norm_quant(const NormAr
 #pragma unroll
         for (int k = 0; k < 32; k += 2) amax[(k >> 1) & 3] = max3_abs(amax[(k >> 1) & 3], v[k], v[k + 1]);
         // ---- row scale; back to layout A
-        const float2 t = reduce.sum_max(ss, fmaxf(fmaxf(amax[0], amax[1]), fmaxf(amax[2], amax[3])));
+        const float2 t = reduce.sum_max(ss, max3_abs(max3_abs(amax[0], amax[1], amax[2]), amax[3], 0.f));
         if (G > 8) {
             __syncwarp();   // one warp per row: the reduction has no barrier
 #pragma unroll
@@ -697,10 +699,12 @@ __global__ void __launch_bounds__(IN == 0 ? 640 : 512) k_norm_quant(const NormAr
                     __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410) ^ 0x88888888u;
             }
         }
-        // a row with a NaN has a NaN scale, also where nothing else is left of it
+        // a NaN or infinity among the rotated values makes the scale NaN: of an infinite
+        // amax and rstd = 0 nothing else would remain of it
         if (threadIdx.x == 0) {
             const float rstd = inv_rms(t.x, a.K, a.eps);
-            a.sx[m] = t.y == 0.f ? (rstd != rstd ? rstd : 0.f) : __fmul_rn(__fmul_rn(__fdiv_rn(t.y, LEVELS), a.cg), rstd);
+            const float sx = t.y == 0.f ? 0.f : __fmul_rn(__fmul_rn(__fdiv_rn(t.y, LEVELS), a.cg), rstd);
+            a.sx[m] = t.y < INFINITY ? sx : NAN;
         }
     }
 }
