@@ -1,9 +1,10 @@
 """The quantiser behind the residual and norm at its edges: rows of infinities in any
-arrangement."""
+arrangement, rows whose largest value is too small for the quantiser's reciprocal."""
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_norm import BF16, F16, hq, rows, weights
+from test_gpu_norm import BF16, F16, F32, U, f32, hq, rows, unpack, weights
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +52,43 @@ def test_scale_of_rows_with_infinities(K, group, xt, bits):
     w2 = w.clone()
     w2[:4] = torch.tensor([INF, INF, INF, -INF])
     assert hq.hq_norm_rotate_quant(H, w2, 1e-5, group, d, bits=bits)[1].isnan().all()
+
+
+def tiny_rows(K, group, amaxes):
+    H = torch.randn(len(amaxes), K, generator=torch.Generator().manual_seed(7))
+    H[:, 0] = 2.0 * group                   # no rotated value of the first group is zero
+    H[:, group:2 * group] = 0               # those of the second are, where there is one
+    return (H / H.abs().amax(1, keepdim=True) * torch.tensor(amaxes)[:, None] / 2).to(BF16)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("K,group", [(64, 8), (128, 128), (2048, 512), (4096, 4096)])
+def test_rows_too_small_for_the_reciprocal(K, group, bits):
+    """Where 7 / amax is infinite the clamp decides: the largest code with the value's
+    sign, 0 for a zero.  Rows on both sides of that, bf16 subnormals among them."""
+    top = 7 if bits == 4 else 127
+    amaxes = [3e-40, 1e-39, 1e-38, 2e-38, 3e-38, 1e-37, 3.5e-37, 4e-37, 1e-36]
+    H = tiny_rows(K, group, amaxes).cuda()
+    w = torch.ones(K, dtype=F32, device="cuda")
+    Xq, sx, _, _ = hq.hq_norm_rotate_quant(H, w, 1e-5, group, bits=bits)
+    q = unpack(Xq, bits).astype(np.int64)
+    u = f32(H)
+    s = 1
+    while s < group:
+        t = u.reshape(len(amaxes), K // (2 * s), 2, s)
+        u = np.stack((t[:, :, 0] + t[:, :, 1], t[:, :, 0] - t[:, :, 1]), 2).reshape(len(amaxes), K)
+        s *= 2
+    amax = np.abs(u).max(1)
+    assert u.dtype == np.float32 and (amax > 0).all()
+    with np.errstate(over="ignore"):
+        inv = np.float32(top) / amax
+    assert np.isinf(inv).any() and np.isfinite(inv).any()
+    for m in range(len(amaxes)):
+        if np.isinf(inv[m]):
+            want = np.sign(u[m]).astype(np.int64) * top
+        else:
+            want = np.clip(np.rint(u[m] * inv[m]), -top, top).astype(np.int64)
+        assert np.array_equal(q[m], want), (m, inv[m], q[m][:8], want[:8])
+    want = (amax / np.float32(top)).astype(np.float32) * np.float32(1 / np.sqrt(group))
+    want = want.astype(np.float64) / np.sqrt(1e-5)
+    assert (np.abs(sx.cpu().numpy() - want) <= 34 * U * want + 2.0 ** -149 * 400).all()
