@@ -81,7 +81,8 @@ size_t hq_packed_weight_bytes(int64_t N, int64_t K);
  *   amax = max over the whole row of |u|
  *   q = clamp(rint(fl32(u * fl32(7/amax))), -7, 7)   (all 0 if amax == 0)
  *   sx[m] = fl32(fl32(amax/7) * fl32(1/sqrt(group)))  (0 if amax == 0)
- * so that x*blockdiag(H)/sqrt(group) ~= q * sx[m].  H = diag(d)*Sylvester is a
+ * (where fl32(7/amax) is infinite, amax <= 7 * 2^-128, q is 7 with the sign of u, 0 for
+ * u = 0) so that x*blockdiag(H)/sqrt(group) ~= q * sx[m].  H = diag(d)*Sylvester is a
  * Hadamard matrix with H[0,:] = 1 when d[0] = +1.
  *
  *  X       device, [M][ld_x] elements of type xt (HQ_F16 or HQ_BF16), row-major
@@ -562,8 +563,8 @@ hq_status hq_residual_norm(const void* H, int64_t ld_h, const void* Y, int64_t l
  *   u = (v .* d) * H_sylv            as hq_rotate_quant
  *   q = clamp(rint(fl32(u * fl32(7/amax))), -7, 7),  amax = max |u| of the row
  *   sx = fl32(fl32(fl32(amax/7) * fl32(1/sqrt(group))) * r(h))
- * (127 in place of 7 for bits = 8; where fl32(7/amax) is infinite, amax below about
- * 2e-38, q is 7 with the sign of u, 0 for u = 0): the codes depend on no sum over the row
+ * (127 in place of 7 for bits = 8; where fl32(7/amax) is infinite, amax <= 7 * 2^-128, q
+ * is 7 with the sign of u, 0 for u = 0): the codes depend on no sum over the row
  * and skip the 16-bit rounding of the normed row that the two calls in
  * sequence have.
  *  H .. eps as hq_residual_norm, xt HQ_F16 or HQ_BF16;  Y, gate, H_out and X may be

@@ -48,6 +48,11 @@ inline bool allow_smem(SmemOptIn& done, Kern kern, int bytes) {
     return true;
 }
 
+// 1 with the sign of u (0 and NaN stay): in place of u where fl(LEVELS / amax) is
+// infinite, which is amax <= LEVELS 2^-128 (2.1e-38 for 4 bits, 3.7e-37 for 8; bf16 rows
+// only).  LEVELS times it is what the quantiser's clamp makes of the infinite product.
+__device__ __forceinline__ float sign_of(float u) { return u > 0.f ? 1.f : u < 0.f ? -1.f : u; }
+
 // ------------------------------------------------------------------ mbarrier
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");

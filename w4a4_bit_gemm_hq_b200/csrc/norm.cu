@@ -669,9 +669,9 @@ __global__ void __launch_bounds__(IN == 0 ? 640 : 512) k_norm_quant(const NormAr
         }
         constexpr float LEVELS = BITS == 8 ? 127.0f : 7.0f;
         float inv = __fdiv_rn(LEVELS, t.y);
-        if (inv == INFINITY) {   // amax 0 or below about 2e-38 (4e-37 for 8 bits): of the product the clamp's limits are left
+        if (inv == INFINITY) {   // amax is 0 or tiny
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = v[k] == 0.f ? 0.f : copysignf(1.f, v[k]);
+            for (int k = 0; k < 32; ++k) v[k] = sign_of(v[k]);
             inv = LEVELS;
         }
 #pragma unroll

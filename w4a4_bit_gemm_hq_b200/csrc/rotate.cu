@@ -284,8 +284,15 @@ __global__ void __launch_bounds__(512) k_rotate(const void* __restrict__ X, int6
                 for (int wi = 0; wi < nw; ++wi) amax = fmaxf(amax, red[par][wi]);
                 uint32_t words[4] = {0u, 0u, 0u, 0u};
                 uint32_t bytes[4][2] = {{0u, 0u}, {0u, 0u}, {0u, 0u}, {0u, 0u}};
+                float inv = __fdiv_rn(LEVELS, amax);
+                if (inv == INFINITY) {   // amax is 0 or tiny
+#pragma unroll
+                    for (int ah = 0; ah < 4; ++ah)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) w[ah][e] = sign_of(w[ah][e]);
+                    inv = LEVELS;
+                }
                 if (amax != 0.f && MODE == MODE_QUANT8) {
-                    const float inv = __fdiv_rn(LEVELS, amax);
                     const float2 magic = make_float2(12582912.0f, 12582912.0f);  // 1.5 * 2^23
 #pragma unroll
                     for (int ah = 0; ah < 4; ++ah)
@@ -298,7 +305,6 @@ __global__ void __launch_bounds__(512) k_rotate(const void* __restrict__ X, int6
                                                  << (8 * (e & 2));
                         }
                 } else if (amax != 0.f) {
-                    const float inv = __fdiv_rn(LEVELS, amax);
                     const float2 magic = make_float2(12582912.0f, 12582912.0f);  // 1.5 * 2^23
 #pragma unroll
                     for (int ah = 0; ah < 4; ++ah) {
@@ -442,11 +448,16 @@ __global__ void __launch_bounds__(512) k_rotate(const void* __restrict__ X, int6
                 uint32_t bytes[EPT / 4];
     #pragma unroll
                 for (int j = 0; j < EPT / 4; ++j) bytes[j] = 0u;
+                float inv = __fdiv_rn(LEVELS, amax);
+                if (inv == INFINITY) {   // amax is 0 or tiny
+    #pragma unroll
+                    for (int i = 0; i < EPT / 2; ++i) v[i] = make_float2(sign_of(v[i].x), sign_of(v[i].y));
+                    inv = LEVELS;
+                }
                 if (amax == 0.f) {
     #pragma unroll
                     for (int j = 0; j < EPT / 8; ++j) words[j] = 0u;
                 } else if (MODE == MODE_QUANT8) {
-                    const float inv = __fdiv_rn(LEVELS, amax);
                     const float2 magic = make_float2(12582912.0f, 12582912.0f);  // 1.5 * 2^23
     #pragma unroll
                     for (int j = 0; j < EPT / 4; ++j) {
@@ -460,7 +471,6 @@ __global__ void __launch_bounds__(512) k_rotate(const void* __restrict__ X, int6
     #pragma unroll
                     for (int j = 0; j < EPT / 8; ++j) words[j] = 0u;
                 } else {
-                    const float inv = __fdiv_rn(LEVELS, amax);
                     const float2 magic = make_float2(12582912.0f, 12582912.0f);  // 1.5 * 2^23
     #pragma unroll
                     for (int j = 0; j < EPT / 8; ++j) {

@@ -399,7 +399,6 @@ __global__ void __launch_bounds__(rq::THREADS, 1)
         if (abort_now) break;
 
         // ---- scale, round half to even, pack, store
-        const float inv = amax == 0.f ? 0.f : __fdiv_rn(LEVELS, amax);   // amax == 0: every code is 0
         if constexpr (ASYM) {
             if (act) {
                 float lo4[4], hi4[4];
@@ -470,68 +469,81 @@ __global__ void __launch_bounds__(rq::THREADS, 1)
                 sx[gi] = __fmul_rn(__fdiv_rn(dlt, 15.f), cg);
                 zx[gi] = static_cast<int32_t>(zf);
             }
-        } else if constexpr (Q8) {
-            // the low byte of fl32(fl32(u * inv) + 1.5 * 2^23) is q in two's complement
-            auto b4 = [&](float2 x0, float2 x1) {
-                const float2 r0 = rq_add2(make_float2(__fmul_rn(x0.x, inv), __fmul_rn(x0.y, inv)), mg);
-                const float2 r1 = rq_add2(make_float2(__fmul_rn(x1.x, inv), __fmul_rn(x1.y, inv)), mg);
-                return __byte_perm(__byte_perm(__float_as_uint(r0.x), __float_as_uint(r0.y), 0x0040),
-                                   __byte_perm(__float_as_uint(r1.x), __float_as_uint(r1.y), 0x0040), 0x5410);
-            };
-            if (act) {
-                if constexpr (T == 32) {
-                    // lane l: channels 128 a + 4 l .. + 3 of the warp's group, 4 bytes per a
-                    uint32_t* dst = reinterpret_cast<uint32_t*>(Xq + static_cast<int64_t>(m) * K + 4096 * wt) + lane;
-#pragma unroll
-                    for (int a = 0; a < 32; ++a) dst[32 * a] = b4(wq[0][a], wq[1][a]);
-                } else {
-                    // 128 bytes per thread, 16 at a time
-                    uint4* dst = reinterpret_cast<uint4*>(Xq + static_cast<int64_t>(m) * K + 128 * u);
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        dst[q] = make_uint4(b4(v[8 * q], v[8 * q + 1]), b4(v[8 * q + 2], v[8 * q + 3]),
-                                            b4(v[8 * q + 4], v[8 * q + 5]), b4(v[8 * q + 6], v[8 * q + 7]));
-                }
-            }
-        } else if constexpr (T == 32) {
-            // lane l: 2 bytes (channels 128 a + 4 l .. + 3) per a, 64 contiguous bytes per warp store
-            if (act) {
-                uint16_t* dst = reinterpret_cast<uint16_t*>(Xq + static_cast<int64_t>(m) * (K / 2) + 2048 * wt) + lane;
-#pragma unroll
-                for (int a = 0; a < 32; ++a) {
-                    const float2 x0 = wq[0][a], x1 = wq[1][a];
-                    const float2 r0 = rq_add2(make_float2(__fmul_rn(x0.x, inv), __fmul_rn(x0.y, inv)), mg);
-                    const float2 r1 = rq_add2(make_float2(__fmul_rn(x1.x, inv), __fmul_rn(x1.y, inv)), mg);
-                    const uint32_t b0 = (__float_as_uint(r0.y) << 4) + __float_as_uint(r0.x);
-                    const uint32_t b1 = (__float_as_uint(r1.y) << 4) + __float_as_uint(r1.x);
-                    dst[32 * a] = static_cast<uint16_t>(((b1 << 8) + b0) ^ 0x8888u);
-                }
-            }
         } else {
-            // 64 bytes per thread, 16 at a time
-            if (act) {
-                uint4* dst = reinterpret_cast<uint4*>(Xq + static_cast<int64_t>(m) * (K / 2) + 64 * u);
+            auto store_codes = [&](auto scaled) {   // scaled(u): fl32(u * inv)
+                if constexpr (Q8) {
+                    // the low byte of fl32(fl32(u * inv) + 1.5 * 2^23) is q in two's complement
+                    auto b4 = [&](float2 x0, float2 x1) {
+                        const float2 r0 = rq_add2(scaled(x0), mg);
+                        const float2 r1 = rq_add2(scaled(x1), mg);
+                        return __byte_perm(__byte_perm(__float_as_uint(r0.x), __float_as_uint(r0.y), 0x0040),
+                                           __byte_perm(__float_as_uint(r1.x), __float_as_uint(r1.y), 0x0040), 0x5410);
+                    };
+                    if (act) {
+                        if constexpr (T == 32) {
+                            // lane l: channels 128 a + 4 l .. + 3 of the warp's group, 4 bytes per a
+                            uint32_t* dst = reinterpret_cast<uint32_t*>(Xq + static_cast<int64_t>(m) * K + 4096 * wt) + lane;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t words[4];
+                            for (int a = 0; a < 32; ++a) dst[32 * a] = b4(wq[0][a], wq[1][a]);
+                        } else {
+                            // 128 bytes per thread, 16 at a time
+                            uint4* dst = reinterpret_cast<uint4*>(Xq + static_cast<int64_t>(m) * K + 128 * u);
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        uint32_t P[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            // scalar __fmul_rn: the product is rounded before the rounding
-                            // add (a packed f32x2 multiply here was contracted with the
-                            // add into one fused operation, which rounds exact ties the
-                            // other way)
-                            const float2 x = v[16 * q + 4 * w + e];
-                            const float2 r = rq_add2(make_float2(__fmul_rn(x.x, inv), __fmul_rn(x.y, inv)), mg);
-                            P[e] = (__float_as_uint(r.y) << 4) + __float_as_uint(r.x);   // byte e (low 16 bits)
+                            for (int q = 0; q < 8; ++q)
+                                dst[q] = make_uint4(b4(v[8 * q], v[8 * q + 1]), b4(v[8 * q + 2], v[8 * q + 3]),
+                                                    b4(v[8 * q + 4], v[8 * q + 5]), b4(v[8 * q + 6], v[8 * q + 7]));
                         }
-                        const uint32_t q01 = (P[1] << 8) + P[0], q23 = (P[3] << 8) + P[2];
-                        words[w] = __byte_perm(q01, q23, 0x5410) ^ 0x88888888u;
                     }
-                    dst[q] = make_uint4(words[0], words[1], words[2], words[3]);
+                } else if constexpr (T == 32) {
+                    // lane l: 2 bytes (channels 128 a + 4 l .. + 3) per a, 64 contiguous bytes per warp store
+                    if (act) {
+                        uint16_t* dst = reinterpret_cast<uint16_t*>(Xq + static_cast<int64_t>(m) * (K / 2) + 2048 * wt) + lane;
+#pragma unroll
+                        for (int a = 0; a < 32; ++a) {
+                            const float2 x0 = wq[0][a], x1 = wq[1][a];
+                            const float2 r0 = rq_add2(scaled(x0), mg);
+                            const float2 r1 = rq_add2(scaled(x1), mg);
+                            const uint32_t b0 = (__float_as_uint(r0.y) << 4) + __float_as_uint(r0.x);
+                            const uint32_t b1 = (__float_as_uint(r1.y) << 4) + __float_as_uint(r1.x);
+                            dst[32 * a] = static_cast<uint16_t>(((b1 << 8) + b0) ^ 0x8888u);
+                        }
+                    }
+                } else {
+                    // 64 bytes per thread, 16 at a time
+                    if (act) {
+                        uint4* dst = reinterpret_cast<uint4*>(Xq + static_cast<int64_t>(m) * (K / 2) + 64 * u);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t words[4];
+#pragma unroll
+                            for (int w = 0; w < 4; ++w) {
+                                uint32_t P[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    // scalar __fmul_rn: the product is rounded before the rounding
+                                    // add (a packed f32x2 multiply here was contracted with the
+                                    // add into one fused operation, which rounds exact ties the
+                                    // other way)
+                                    const float2 x = v[16 * q + 4 * w + e];
+                                    const float2 r = rq_add2(scaled(x), mg);
+                                    P[e] = (__float_as_uint(r.y) << 4) + __float_as_uint(r.x);   // byte e (low 16 bits)
+                                }
+                                const uint32_t q01 = (P[1] << 8) + P[0], q23 = (P[3] << 8) + P[2];
+                                words[w] = __byte_perm(q01, q23, 0x5410) ^ 0x88888888u;
+                            }
+                            dst[q] = make_uint4(words[0], words[1], words[2], words[3]);
+                        }
+                    }
                 }
+            };
+            const float inv = amax == 0.f ? 0.f : __fdiv_rn(LEVELS, amax);   // amax == 0: every code is 0
+            if (XT == rq::XT_F16 || __builtin_expect(amax > LEVELS * 0x1p-128f, 1)) {
+                store_codes([&](float2 x) { return make_float2(__fmul_rn(x.x, inv), __fmul_rn(x.y, inv)); });
+            } else {   // bf16 rows may be so small that inv is infinite
+                // (a branch of its own: the signs put into v ahead of one store made bf16 rows of
+                // 4096 x 11008, group 128 take 37.7 us; so they take 32.7, 32.0 without this
+                // branch, and with 8 bits 38.0, 39.5 without it)
+                store_codes([](float2 x) { return make_float2(LEVELS * sign_of(x.x), LEVELS * sign_of(x.y)); });
             }
         }
         if (!ASYM && leader) sx[m] = (amax == 0.f) ? 0.f : __fmul_rn(__fdiv_rn(amax, LEVELS), cg);
