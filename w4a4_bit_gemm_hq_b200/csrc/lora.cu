@@ -426,13 +426,18 @@ struct Tile {
     int a, start, count, live;
 };
 
-__device__ __forceinline__ Tile tile_of(const ExpandArgs& p, int i) {
+__device__ __forceinline__ Tile entry_of(const ExpandArgs& p, int i) {   // without the rank
     Tile t;
     t.a = p.tiles[3 * i];
     t.start = p.tiles[3 * i + 1];
     t.count = p.tiles[3 * i + 2];
     if (t.count <= 0 || t.count > LR_TILE || t.start < 0 || t.start > p.M - t.count || t.a >= p.n) t.count = 0;
     t.live = 0;
+    return t;
+}
+
+__device__ __forceinline__ Tile tile_of(const ExpandArgs& p, int i) {
+    Tile t = entry_of(p, i);
     if (t.count > 0 && t.a >= 0) t.live = p.ranks != nullptr ? min(max(p.ranks[t.a], 0), p.r) : p.r;
     return t;
 }
@@ -464,6 +469,11 @@ __device__ __forceinline__ uint32_t narrow16(bool bf, float a, float b) {
     }
     const __half2 v = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Two entries that one product may take together
+__device__ __forceinline__ bool linked(const Tile& t, const Tile& next) {
+    return t.count == LR_TILE && next.count > 0 && next.a == t.a && next.start == t.start + LR_TILE;
 }
 
 // The tile's rows of Y are its rows of base (or zero): tokens without an adapter
@@ -788,6 +798,7 @@ __global__ void __launch_bounds__(EX_THREADS + 32, 2) k_lora_expand(const Expand
     extern __shared__ uint8_t dyn[];
     __shared__ uint64_t bar_mem;
     __shared__ uint32_t tmem_mem;
+    __shared__ int run_mem[2][EX_THREADS / 32 + 1];
     uint8_t* sm = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const bool mma_warp = warp == EX_THREADS / 32;
@@ -799,26 +810,35 @@ __global__ void __launch_bounds__(EX_THREADS + 32, 2) k_lora_expand(const Expand
     uint8_t* slots = bbuf + 2 * atoms * BATOM;
     float* unscale = reinterpret_cast<float*>(slots + p.depth * BASE);
     const uint32_t bar = smem_u32(&bar_mem);
-    // Tile i takes tile i + 1 along if they are the 2 k-th and the 2 k + 1-st of one
-    // adapter (only an adapter's last tile is not full)
+    // In a run of linked tiles (an adapter's, in a plan as hq_lora_plan makes it) the 2 k-th
+    // takes the 2 k + 1-st along.  Every tile finds where its run begins: the last
+    // place up to its own without a link to the one before (tile 0 has none).
     const int ti = blockIdx.y;
+    auto begins = [&](int i) { return i >= 0 && (i == 0 || !linked(entry_of(p, i - 1), entry_of(p, i))); };
+    const Tile next = entry_of(p, min(ti + 1, p.ntiles - 1));
+    bool here = begins(ti - tid);   // asked for with the tile itself
     const Tile t = tile_of(p, ti);
     if (t.live == 0) {   // the same for the whole CTA
         griddep_wait();
         copy_cols<YT>(p, t, blk0 * EX_NB, (blk1 - blk0) * EX_NB);
         return;
     }
-    int before = 0;
-    for (int i = ti - 1 - tid; i >= 0; i -= EX_THREADS + 32) before ^= p.tiles[3 * i] == t.a;
-    if (__syncthreads_count(before) & 1) {
+    constexpr int WARPS = EX_THREADS / 32 + 1;
+    int first;
+    for (int i = ti - tid, par = 0;; par ^= 1) {
+        const unsigned w = __ballot_sync(0xFFFFFFFFu, here);
+        if (lane == 0) run_mem[par][warp] = w != 0 ? i - (__ffs(w) - 1) : -1;
+        __syncthreads();
+        first = __reduce_max_sync(0xFFFFFFFFu, lane < WARPS ? run_mem[par][lane] : -1);
+        if (first >= 0) break;
+        i -= 32 * WARPS;
+        here = begins(i);
+    }
+    if ((ti - first) & 1) {
         griddep_wait();
         return;
     }
-    int rows = t.count;
-    if (rows == LR_TILE && ti + 1 < p.ntiles) {
-        const Tile n = tile_of(p, ti + 1);
-        if (n.a == t.a && n.count > 0 && n.start == t.start + rows) rows += n.count;
-    }
+    const int rows = t.count + (linked(t, next) ? next.count : 0);   // the last tile is not linked to itself
     if (mma_warp) {
         tmem_alloc(smem_u32(&tmem_mem), 2 * EX_NB);
         tmem_relinquish();
