@@ -662,21 +662,57 @@ class W4A4Linear:
 
     def set_adapters(self, A, B, ranks=None, scales=None):
         """Low-rank adapters beside the layer (hq_lora_apply): A [n, r_max, K] on the
-        layer's input, B [n, N, r_max], 16-bit; None takes them away."""
+        layer's input, B [n, N, r_max], 16-bit; None takes them away.  What no call
+        could use is refused here."""
         if A is None:
             self.adapters = None
             return
         if A.dim() != 3 or A.shape[2] != self.K or B.shape != (A.shape[0], self.N, A.shape[1]):
             raise ValueError("A must be [n, r_max, %d] and B [n, %d, r_max]" % (self.K, self.N))
+        n, r, _ = A.shape
+        if A.dtype not in (torch.float16, torch.bfloat16) or r % 8 or not 0 < r <= 256 or n > 1022:
+            raise ValueError("A and B must be 16-bit, r_max a multiple of 8 up to 256, n at most 1022")
+        dev = A.get_device()
+        _whole(A, "A", dev, A.shape, A.dtype)
+        _whole(B, "B", dev, B.shape, A.dtype)
+        if ranks is not None:
+            _whole(ranks, "ranks", dev, (n,), torch.int32)
+        if scales is not None:
+            _whole(scales, "scales", dev, (n,), torch.float32)
+        if A.data_ptr() % 16 or B.data_ptr() % 16:
+            raise ValueError("A and B must be 16-byte aligned")
         self.adapters = (A, B, ranks, scales)
+
+    def _check(self, X, plan):
+        """Refuses rows and plans before anything runs on them."""
+        dev = _device(X, "the layer's input")
+        if X.dim() != 2 or X.shape[1] != self.K:
+            raise ValueError("the layer's input must be [M, %d]" % self.K)
+        if plan is not None:
+            if self.adapters is None:
+                raise ValueError("the layer has no adapters (set_adapters)")
+            A, M = self.adapters[0], X.shape[0]
+            if A.get_device() != dev or A.dtype is not X.dtype:
+                raise ValueError("the adapters must have the type and device of the layer's input")
+            order, tiles = plan
+            _whole(order, "the plan's order", dev, (M,), torch.int32)
+            _whole(tiles, "the plan's tiles", dev, (hq_lora_max_tiles(M, A.shape[0]), 3), torch.int32)
 
     def _adapted(self, X, plan, Y):
         if plan is None:
             return Y
-        if self.adapters is None:
-            raise ValueError("the layer has no adapters (set_adapters)")
         A, B, ranks, scales = self.adapters
-        return hq_lora_apply(X, A, B, plan[0], plan[1], ranks, scales, base=Y, Y=Y)
+        dev, M = X.get_device(), X.shape[0]      # adapters and plan are checked (set_adapters, _check)
+        n, r, K = A.shape
+        ld_x, ld_y = _rows(X, "X", dev, X.shape, A.dtype), _rows(Y, "Y", dev, (M, self.N), Y.dtype)
+        work = torch.empty((M, r), dtype=torch.float32, device=X.device)
+        p_y = Y.data_ptr()
+        _launch(dev, lib.hq_lora_apply, "hq_lora_apply",
+                (X.data_ptr(), dtype_code(A.dtype), M, K, ld_x, A.data_ptr(), B.data_ptr(), self.N, n, r,
+                 ranks.data_ptr() if ranks is not None else None, scales.data_ptr() if scales is not None else None,
+                 plan[0].data_ptr(), plan[1].data_ptr(), p_y, ld_y, p_y, dtype_code(Y.dtype), ld_y,
+                 work.data_ptr(), 4 * M * r))
+        return Y
 
     def _linear(self, Xq, sx, Y):
         gemm = w4a8_linear if self.act_bits == 8 else w4a4_linear
@@ -686,6 +722,7 @@ class W4A4Linear:
     def forward(self, X, Y=None, Xq=None, sx=None, plan=None):
         """Y [M, N] of the rows X.  plan = hq_lora_plan(ids, n) adds the adapters of
         the tokens."""
+        self._check(X, plan)
         if self.offq:
             Xq, sx, zx = hq_rotate_quant_asym(X, self.group, self.H_signs, Xq, sx)
             Y = w4a4_linear_asym(Xq, sx, zx, self.Wq, self.sw, self.zw, self.gw, self.Rq, self.sr,
@@ -702,7 +739,18 @@ class W4A4Linear:
         updated with the previous block's output, and that stream
         (hq_residual_norm; H itself without a block).  One launch makes the codes
         from the stream (hq_norm_rotate_quant); with a norm after the block, or
-        OffQ activations, the normed rows are written and quantised from memory."""
+        OffQ activations, the normed rows are written and quantised from memory.
+        A refused call leaves the stream as it was."""
+        self._check(H, plan)
+        if H.dtype not in (torch.float16, torch.bfloat16):
+            raise ValueError("the residual stream must be 16-bit")
+        if self.Wq.get_device() != H.get_device():
+            raise ValueError("the layer and the residual stream must be on one device")
+        if Y is not None:
+            _whole(Y, "Y", H.get_device(), (H.shape[0], self.N), Y.dtype)
+            if Y.data_ptr() % 16:
+                raise ValueError("Y must be 16-byte aligned")
+            dtype_code(Y.dtype)
         if self.offq or w_post is not None:
             H_out, X = hq_residual_norm(H, w, eps, block, w_post, gate, alpha, w_offset, H_out)
             Y = self.forward(X, Y, plan=plan)
