@@ -1,6 +1,6 @@
 """W4A4Linear refuses a call before anything of it runs: the residual stream, which
 forward_normed updates (in place, where the caller asks for it), must not be changed
-by a call that is then refused.
+by a call that is then refused.  And the whole call runs on its input's device.
 On the CPU: the library's calls are replaced by recorders."""
 import contextlib
 
@@ -46,7 +46,7 @@ def calls(hq, monkeypatch):
     def record(name, result):
         def call(*a, **kw):
             log.append((name, current[0]))
-            return result
+            return result() if callable(result) else result
         monkeypatch.setattr(hq, name, call)
 
     @contextlib.contextmanager
@@ -55,19 +55,20 @@ def calls(hq, monkeypatch):
         yield
         current[0] = before
 
-    x, codes = OnDevice(torch.zeros(M, K, dtype=F16)), OnDevice(torch.zeros(M, K // 2, dtype=torch.uint8))
-    y = OnDevice(torch.zeros(M, N, dtype=F16))
-    record("hq_norm_rotate_quant", (codes, None, x, x))
-    record("hq_residual_norm", (x, x))
-    record("hq_rotate_quant", (codes, None))
-    record("hq_rotate_quant_asym", (codes, None, None))
+    x = lambda: OnDevice(torch.zeros(M, K, dtype=F16), current[0])                     # noqa: E731
+    codes = lambda: OnDevice(torch.zeros(M, K // 2, dtype=torch.uint8), current[0])    # noqa: E731
+    y = lambda: OnDevice(torch.zeros(M, N, dtype=F16), current[0])                     # noqa: E731
+    record("hq_norm_rotate_quant", lambda: (codes(), None, x(), x()))
+    record("hq_residual_norm", lambda: (x(), x()))
+    record("hq_rotate_quant", lambda: (codes(), None))
+    record("hq_rotate_quant_asym", lambda: (codes(), None, None))
     record("w4a4_linear", y)
     record("w4a4_linear_asym", y)
     record("_launch", None)
     monkeypatch.setattr(hq.torch, "empty", lambda shape, dtype=None, device=None: torch.zeros(shape, dtype=dtype))
     record("hq_linear_workspace_size", 0)
     monkeypatch.setattr(hq.torch.cuda, "device", device)
-    monkeypatch.setattr(hq.torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(hq.torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
     return log
 
 
@@ -181,3 +182,14 @@ def test_a_refused_call_leaves_the_stream(hq, post):
     assert torch.equal(H, kept)
     out, h = layer.forward_normed(H, w, 1e-5, plan=plan, **kw)
     assert h is H and not torch.equal(H, kept) and out.isfinite().all()
+
+
+@pytest.mark.parametrize("kind", ["fused", "post", "offq"])
+def test_every_launch_is_on_the_device_of_the_rows(hq, calls, kind):
+    layer = layer_of(hq, kind == "offq", dev=1)
+    layer.set_adapters(*adapters(dev=1))
+    H, w = OnDevice(torch.zeros(M, K, dtype=F16), 1), OnDevice(torch.zeros(K, dtype=F16), 1)
+    layer.forward_normed(H, w, 1e-5, block=H, w_post=w if kind == "post" else None, plan=plan_of(hq, dev=1))
+    layer.forward(H, plan=plan_of(hq, dev=1))
+    assert len(launches(calls)) >= 6 and all(d == 1 for _, d in launches(calls))
+    assert hq.torch._C._cuda_getDevice() == 0

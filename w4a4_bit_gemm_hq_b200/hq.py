@@ -684,7 +684,7 @@ class W4A4Linear:
         self.adapters = (A, B, ranks, scales)
 
     def _check(self, X, plan):
-        """Refuses rows and plans before anything runs on them."""
+        """Refuses rows and plans before anything runs on them; the device they are on."""
         dev = _device(X, "the layer's input")
         if X.dim() != 2 or X.shape[1] != self.K:
             raise ValueError("the layer's input must be [M, %d]" % self.K)
@@ -697,6 +697,7 @@ class W4A4Linear:
             order, tiles = plan
             _whole(order, "the plan's order", dev, (M,), torch.int32)
             _whole(tiles, "the plan's tiles", dev, (hq_lora_max_tiles(M, A.shape[0]), 3), torch.int32)
+        return dev
 
     def _adapted(self, X, plan, Y):
         if plan is None:
@@ -722,7 +723,10 @@ class W4A4Linear:
     def forward(self, X, Y=None, Xq=None, sx=None, plan=None):
         """Y [M, N] of the rows X.  plan = hq_lora_plan(ids, n) adds the adapters of
         the tokens."""
-        self._check(X, plan)
+        dev = self._check(X, plan)
+        if torch._C._cuda_getDevice() != dev:        # every launch is on the device of X
+            with torch.cuda.device(dev):
+                return self.forward(X, Y, Xq, sx, plan)
         if self.offq:
             Xq, sx, zx = hq_rotate_quant_asym(X, self.group, self.H_signs, Xq, sx)
             Y = w4a4_linear_asym(Xq, sx, zx, self.Wq, self.sw, self.zw, self.gw, self.Rq, self.sr,
@@ -741,13 +745,16 @@ class W4A4Linear:
         from the stream (hq_norm_rotate_quant); with a norm after the block, or
         OffQ activations, the normed rows are written and quantised from memory.
         A refused call leaves the stream as it was."""
-        self._check(H, plan)
+        dev = self._check(H, plan)
+        if torch._C._cuda_getDevice() != dev:
+            with torch.cuda.device(dev):
+                return self.forward_normed(H, w, eps, block, w_post, gate, alpha, w_offset, Y, H_out, plan)
         if H.dtype not in (torch.float16, torch.bfloat16):
             raise ValueError("the residual stream must be 16-bit")
-        if self.Wq.get_device() != H.get_device():
+        if self.Wq.get_device() != dev:
             raise ValueError("the layer and the residual stream must be on one device")
         if Y is not None:
-            _whole(Y, "Y", H.get_device(), (H.shape[0], self.N), Y.dtype)
+            _whole(Y, "Y", dev, (H.shape[0], self.N), Y.dtype)
             if Y.data_ptr() % 16:
                 raise ValueError("Y must be 16-byte aligned")
             dtype_code(Y.dtype)
