@@ -528,8 +528,10 @@ hq_status hq_mxfp4_linear(const uint8_t* Xq, const uint8_t* sx, int64_t M, int64
  *   p = fl(gate * p)                                   (gate given)
  *   h = e(fl(H + fl(alpha * p)))                       (h = H when Y is NULL)
  *   X = e(fl(fl(h * fl(w + w_offset)) * r(h)))         (w given)
- * with r(v) = 1 / sqrt(sum v^2 / K + eps), the sum in fp32 (|v| below 1e18; eps = 0
- * makes X NaN where a row is zero).
+ * with r(v) = 1 / sqrt(sum v^2 / K + eps).  The sum is held in fp32, by fused adds of the
+ * squares: rows need sum v^2 < 3.4e38, which |v| < 1.4e17 gives for any K (larger finite
+ * rows have r = 0).  eps = 0 makes X NaN where a row is zero, and leaves infinities
+ * where all its squares vanish (|v| below 1e-23).
  *  H        device, [M][ld_h] residual stream
  *  Y        device, [M][ld_y] the block's output, or NULL (no block: H is normed)
  *  xt       type of H, Y, gate, H_out and X: HQ_F16, HQ_BF16 or HQ_F32

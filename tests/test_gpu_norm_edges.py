@@ -1,14 +1,32 @@
-"""The quantiser behind the residual and norm at its edges: rows of infinities in any
-arrangement, rows whose largest value is too small for the quantiser's reciprocal."""
+"""The residual / norm / quantiser calls at their edges: rows of infinities in any
+arrangement, rows whose largest value is too small for the quantiser's reciprocal, the
+largest rows the fp32 sum of squares has room for.  Tolerances as derived in
+test_gpu_norm."""
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_norm import BF16, F16, F32, U, f32, hq, rows, unpack, weights
+from test_gpu_norm import BF16, F16, F32, U, codes_fp32, f32, half_step, hq, inv_rms, rows, unpack, weights
 
 pytestmark = pytest.mark.gpu
 
 NAN, INF = float("nan"), float("inf")
+
+
+def holes(M, K, dt, pad=0):
+    """[M, K] view of a buffer full of NaN, rows on 16 bytes."""
+    return torch.full((M, -(-K // 8) * 8 + pad), NAN, dtype=dt, device="cuda")[:, :K]
+
+
+def within(got, want, tol):
+    err = (got.double() - want).abs()
+    assert (err <= tol).all(), ((~(err <= tol)).sum(), (err / tol).max())
+
+
+def check_x(x, h, w, off, eps):
+    want = h.double() * (w.double() + off) * inv_rms(h.double(), eps)
+    tol = 33 * U * want.abs()
+    within(x, want, tol + half_step(want.abs() + tol, h.dtype))
 
 
 @pytest.mark.parametrize("bits", [4, 8])
@@ -92,3 +110,23 @@ def test_rows_too_small_for_the_reciprocal(K, group, bits):
     want = (amax / np.float32(top)).astype(np.float32) * np.float32(1 / np.sqrt(group))
     want = want.astype(np.float64) / np.sqrt(1e-5)
     assert (np.abs(sx.cpu().numpy() - want) <= 34 * U * want + 2.0 ** -149 * 400).all()
+
+
+@pytest.mark.parametrize("K", [4096, 16384])
+@pytest.mark.parametrize("xt", [BF16, F32])
+def test_rows_as_large_as_the_sum_of_squares_allows(xt, K):
+    """sum v^2 just below the largest fp32 number (3.4028e38)."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    size = (0.98 * 3.4028e38 / K) ** 0.5
+    H = torch.where(torch.rand(3, K, generator=g, device="cuda") < 0.5, -size, size).to(xt)
+    H = torch.where(H.double().abs() > size, H * 0.99, H).to(xt)      # a rounding up of the type taken back
+    H[1, ::2] = 0
+    assert (H.double().square().sum(1) < 3.4028e38).all()
+    w = weights(K, F32, 2)
+    x = hq.hq_residual_norm(H, w, 1e-5, X=holes(3, K, xt))[1]
+    check_x(x, H, w, 0.0, 1e-5)
+    if xt != F32:
+        sx = hq.hq_norm_rotate_quant(H, w, 1e-5, 128)[1]
+        _, _, amax = codes_fp32(H, None, None, 1.0, w, 0.0, 128, None, 4)
+        want = amax.astype(np.float64) / 7 / np.sqrt(128) * inv_rms(H.double(), 1e-5)[:, 0].cpu().numpy()
+        assert (np.abs(sx.cpu().numpy() - want) <= 34 * U * want).all()
