@@ -626,7 +626,7 @@ hq_status hq_lora_plan(const int32_t* ids, int64_t M, int64_t n, int32_t* order,
  * equal to Y with another stride), HQ_ERR_ALIGN, HQ_ERR_UNSUPPORTED (the limits
  * above, fp32 X), HQ_ERR_CUDA.  M == 0 or N == 0 is a no-op.
  */
-size_t hq_lora_workspace_size(int64_t M, int32_t r_max);
+size_t hq_lora_workspace_size(int64_t M, int32_t r_max);   /* SIZE_MAX where the size does not fit */
 hq_status hq_lora_apply(const void* X, hq_dtype xt, int64_t M, int64_t K, int64_t ld_x, const void* A, const void* B,
                         int64_t N, int64_t n, int32_t r_max, const int32_t* ranks, const float* scales,
                         const int32_t* order, const int32_t* tiles, const void* base, int64_t ld_b, void* Y,

@@ -1287,7 +1287,7 @@ using namespace hq;
 
 extern "C" int64_t hq_lora_max_tiles(int64_t M, int64_t n) {
     if (M <= 0 || n < 0) return 0;
-    return M / LR_TILE + (n + 1 < M ? n + 1 : M);
+    return M / LR_TILE + (n < M ? n + 1 : M);
 }
 
 extern "C" hq_status hq_lora_plan(const int32_t* ids, int64_t M, int64_t n, int32_t* order, int32_t* tiles,
@@ -1327,7 +1327,8 @@ extern "C" hq_status hq_lora_plan(const int32_t* ids, int64_t M, int64_t n, int3
 
 extern "C" size_t hq_lora_workspace_size(int64_t M, int32_t r_max) {
     if (M <= 0 || r_max <= 0) return 0;
-    return static_cast<size_t>(M) * r_max * sizeof(float);
+    const size_t row = static_cast<size_t>(r_max) * sizeof(float);
+    return static_cast<size_t>(M) > SIZE_MAX / row ? SIZE_MAX : M * row;
 }
 
 extern "C" hq_status hq_lora_apply(const void* X, hq_dtype xt, int64_t M, int64_t K, int64_t ld_x, const void* A,
