@@ -617,13 +617,14 @@ hq_status hq_lora_plan(const int32_t* ids, int64_t M, int64_t n, int32_t* order,
  *           HQ_ERR_ARG in the device status word.
  *  base     device, [M][ld_b] of type yt (the layer's output), or NULL: zero.  May
  *           be Y itself (same stride).
- *  Y        device, [M][ld_y] of type yt: HQ_F16, HQ_BF16 or HQ_F32 (output)
+ *  Y        device, [M][ld_y] of type yt: HQ_F16, HQ_BF16 or HQ_F32 (output).  May be X
+ *           itself (rows equally far apart).
  *  workspace, ws_bytes   device scratch of hq_lora_workspace_size(M, r_max) bytes,
  *           in use until the call's work on the stream is done
  * Requirements: K % 8 == 0, N % 8 == 0; X, A, B, base, Y and workspace 16-byte
  * aligned, row strides multiples of 16 bytes (HQ_ERR_ALIGN).
- * Errors: HQ_ERR_ARG (sizes, types, strides, NULLs, a workspace too small, base
- * equal to Y with another stride), HQ_ERR_ALIGN, HQ_ERR_UNSUPPORTED (the limits
+ * Errors: HQ_ERR_ARG (sizes, types, strides, NULLs, a workspace too small, base or
+ * X equal to Y with another stride), HQ_ERR_ALIGN, HQ_ERR_UNSUPPORTED (the limits
  * above, fp32 X), HQ_ERR_CUDA.  M == 0 or N == 0 is a no-op.
  */
 size_t hq_lora_workspace_size(int64_t M, int32_t r_max);   /* SIZE_MAX where the size does not fit */

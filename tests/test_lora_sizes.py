@@ -36,3 +36,12 @@ def test_sizes_beyond_the_limits_are_refused(lib, M, n):
     assert lib.hq_lora_plan(P, M, n, ct.c_void_p(32), ct.c_void_p(48), None) == UNSUPPORTED
     got = lib.hq_lora_apply(P, 0, M, 256, 256, P, P, 128, n, 16, None, None, P, P, None, 0, P, 0, 128, P, 1 << 62, None)
     assert got == UNSUPPORTED
+
+
+def test_results_over_the_input_with_another_stride_are_refused(lib):
+    """Rows of Y over other tokens' rows of X, which may still be read."""
+    def call(X, Y, ld_x, ld_y, yt):
+        return lib.hq_lora_apply(X, 0, 4, 256, ld_x, P, P, 128, 3, 16, None, None, P, P, None, 0, Y, yt, ld_y, P, 1 << 20, None)
+    X = ct.c_void_p(4096)
+    assert call(X, X, 256, 128, 0) == ARG and call(X, X, 256, 264, 0) == ARG
+    assert call(X, X, 256, 256, 2) == ARG                 # fp32 rows are twice as far apart

@@ -1351,6 +1351,7 @@ extern "C" hq_status hq_lora_apply(const void* X, hq_dtype xt, int64_t M, int64_
     if (!lr_al16(X) || !lr_al16(A) || !lr_al16(B) || !lr_al16(Y) || !lr_al16(base) || !lr_al16(workspace) ||
         ld_x * 2 % 16 != 0 || ld_y * es % 16 != 0 || (base && ld_b * es % 16 != 0))
         return HQ_ERR_ALIGN;
+    if (X == Y && ld_x * 2 != ld_y * es) return HQ_ERR_ARG;   // rows of Y over other rows of X
     ShrinkArgs s = {};
     s.X = static_cast<const uint16_t*>(X);
     s.A = static_cast<const uint16_t*>(A);
