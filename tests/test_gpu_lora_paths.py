@@ -129,3 +129,17 @@ def test_terms_of_t_in_an_fp32_result(r, xt):
         assert torch.equal(bf16_terms(t, 3), t.double())
         two = (bf16_terms(t, 2) - t.double()).abs()
         assert (two > 2 * tol * t.abs()).any()
+
+
+@pytest.mark.parametrize("M,n,r", [(300, 40, 32), (300, 40, 96), (700, 2, 32), (700, 2, 128)])
+def test_over_the_input(M, n, r):
+    """K = N and the result written over X, in every form."""
+    d = batch(M, 264, 264, n, r, BF16, BF16, seed=4, ragged=True, runs=50)
+    d["base"] = None
+    want = apply(d, out_dtype=BF16)
+    check(want, d, base=False)
+    X = torch.full((M + 2, 272), 9.0, dtype=BF16, device="cuda")
+    X[:M, :264] = d["X"]
+    d["X"] = X[:M, :264]
+    assert apply(d, Y=d["X"]) is d["X"]
+    assert torch.equal(d["X"], want) and (X[M:] == 9).all() and (X[:, 264:] == 9).all()
