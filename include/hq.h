@@ -523,7 +523,7 @@ hq_status hq_mxfp4_linear(const uint8_t* Xq, const uint8_t* sx, int64_t M, int64
 /*
  * hq_residual_norm -- the residual stream updated with a block's output and the
  * norm the next layer reads.  Per row of K channels, in fp32, every product
- * and sum rounded on its own, e() rounding to the type xt:
+ * and sum of the lines below rounded on its own, e() rounding to the type xt:
  *   p = Y | fl(fl(Y * fl(w_post + w_offset)) * r(Y))   (w_post NULL | given)
  *   p = fl(gate * p)                                   (gate given)
  *   h = e(fl(H + fl(alpha * p)))                       (h = H when Y is NULL)
@@ -603,8 +603,11 @@ hq_status hq_lora_plan(const int32_t* ids, int64_t M, int64_t n, int32_t* order,
 /*
  * hq_lora_apply -- low-rank adapters beside a layer:
  *   Y[m] = base[m] + scales[a] (X[m] A_a^T) B_a^T,  a = the token's adapter,
- * over the adapter's own rank; Y[m] = base[m] for a token without one.  The
- * inner product is summed and kept in fp32; Y is rounded once.
+ * over the adapter's own rank; Y[m] = base[m] for a token without one.  Both
+ * products are summed in fp32, Y is rounded once.  t = scales[a] (X[m] A_a^T) enters the
+ * second product as fp32 in small batches, else as 16-bit terms: to 2^-18 of itself
+ * for HQ_BF16 operands and a 16-bit Y, whole for an fp32 Y, to 2^-22 for HQ_F16 operands.
+ * A token's last bits may so depend on the batch it is in.
  *  X        device, [M][ld_x] the layer's input (before rotation), HQ_F16 or HQ_BF16
  *  A, B     device, [n][r_max][K] and [n][N][r_max], of X's type
  *  r_max    a multiple of 8, up to 256

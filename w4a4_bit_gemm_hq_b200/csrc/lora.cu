@@ -7,13 +7,18 @@
 // the order into tiles of at most 64 tokens of one adapter, so that each
 // adapter's matrices are read once per tile and a tile's product is dense.
 // k_lora_shrink forms t = s_a X A_a^T (fp32, rank r) per tile, k_lora_expand
-// adds t B_a^T to the base rows; where tiles hold few tokens (M < 16 tiles: decode)
-// k_lora_few does both in one launch.  They do at most 2 r flops per element of X
-// and of Y, so for r <= 64 the floor is HBM's: X, base and Y once, and the
-// matrices of the adapters in use.  Measured, GPU time: 1 token 4096 -> 11008,
-// rank 16: 5.8 us; 16 tokens of 16 adapters, rank 32: 9.4 us (1.4 at HBM's rate);
-// 2048 x 4096 -> 4096, rank 32: 25 us (7.8); 8192 x 8192 -> 28672, rank 64: 242 us
-// (170).
+// adds t B_a^T to the base rows; where the batch has fewer than 16 tokens for each
+// tile that its plan may hold (decode; also prompts beside many resident adapters,
+// see launch_lora_y) k_lora_few does both in one launch.  They do at most 2 r flops
+// per element of X and of Y, so for r <= 64 the floor is HBM's: X, base and Y once,
+// and the matrices of the adapters in use.  Measured, GPU time: 1 token 4096 ->
+// 11008, rank 16: 5.9 us; 16 tokens of 16 adapters, rank 32: 9.4 us (1.4 at HBM's
+// rate); 2048 x 4096 -> 4096, rank 32: 24.8 us (7.8); 8192 x 8192 -> 28672, rank 64:
+// 242 us (170).  Above rank 64 the shrink reads X once for every 64 rank positions:
+// 2048 x 4096 -> 4096, rank 128 45 us (10); 8192 x 4096 -> 11008, rank 256 208 us (70).
+// Accumulators are the tensor cores' fp32, which truncates, but plain fp32 in the
+// second product of the few-token forms: the last bits of a token may differ with the
+// batch it comes in.
 #include <cstdint>
 #include <type_traits>
 
@@ -604,7 +609,7 @@ __global__ void __launch_bounds__(FEW_THREADS) k_lora_expand_few(const ExpandArg
 // the latency of its chain of loads and barriers: threads of their own load their
 // columns' B and the first token's base while t is formed, those that form it
 // have theirs prefetched into L2.  Ranks up to 64; t has no place in memory.
-// Against the two kernels (5.9 and 9.6 us for 1 and 16 tokens) it takes 5.8 and 9.4
+// Against the two kernels (5.9 and 9.6 us for 1 and 16 tokens) it took 5.8 and 9.4
 // us, and one launch less of host time (2.5 us), which is what a step of single
 // calls waits for.
 template <int RC>
@@ -738,8 +743,10 @@ __global__ void __launch_bounds__(few_threads<RC>) k_lora_few(const ShrinkArgs s
 // are operands of tcgen05.mma (kind::f16, 128 x 64, fp32 accumulators in tensor
 // memory), so that the warps are left with what HBM sees: base in, Y out.
 //  * t enters as 16-bit terms: with bf16 B two bf16 terms for a 16-bit Y (2^-18
-//    of t, far below Y's rounding) and three for an fp32 Y; with fp16 B two
-//    fp16 terms (2^-22) of the row scaled by a power of two to below 2^14.
+//    of t, far below Y's rounding) and three for an fp32 Y (all of t's 24 bits); with
+//    fp16 B two fp16 terms (2^-22, four times fp32's half step, for an fp32 Y too: a
+//    third would be half as many products again) of the row scaled by a power of two
+//    to below 2^14.
 //  * operands are K-major rows of 128 bytes (64 rank positions) in the 128-byte
 //    swizzle; rows of B are staged in the order that makes MMA column 8 i +
 //    2 t + e of each 32 the output column 8 t + 2 i + e: a lane of the
@@ -1189,7 +1196,8 @@ hq_status launch_expand(ExpandArgs a, int tiles, cudaStream_t st) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const int atoms = (a.r + 63) / 64;
-    // tiles of few tokens, or (bf16 with fp32 Y above rank 192) too much for shared memory
+    // few tokens for each possible tile (see launch_lora_y), or (bf16 with fp32 Y above rank
+    // 192) too much for shared memory: 2048 x 4096 -> 4096, rank 256 takes 787 us so
     if (a.M < 16 * tiles || ex_smem(BF, YT, atoms, 1) > kMaxDynSmem) {
         cfg.gridDim = dim3((a.N + FEW_COLS - 1) / FEW_COLS, tiles);
         cfg.blockDim = dim3(FEW_THREADS);
@@ -1210,11 +1218,12 @@ hq_status launch_expand(ExpandArgs a, int tiles, cudaStream_t st) {
     a.depth = 3;
     // Where every SM is sure to have a CTA, two of them per SM are worth more than blocks
     // asked for ahead (fp32 Y, 8192 x 4096 -> 11008, rank 32: fp16 173 us in place of 185,
-    // bf16 166 and 162; 2024 x 168 -> 1320: 17.1, 19.2), and where shared memory has room
-    // for one only (ranks above 64), one round of larger CTAs more than two of smaller ones
-    // (2048 x 4096 -> 4096, rank 128: 45 us, 48.7; 8192 x 4096 -> 11008, rank 256: 207,
-    // 219).  With fewer CTAs it is the other way round (442 tokens of one adapter, 184 ->
-    // 3864, fp32 Y: 22 in place of 16 us when it was tried, 14 now).
+    // but bf16 166 of 162; 2024 x 168 -> 1320: 17.1, 19.2), and where shared memory has
+    // room for one only (ranks above 64), one round of larger CTAs more than two of smaller
+    // ones (2048 x 4096 -> 4096, rank 128: 45 us, 48.7, but with fp32 Y 67.5 of 66; 8192 x
+    // 4096 -> 11008, rank 256: 207, 219).  With fewer CTAs it is the other way round (442
+    // tokens of one adapter, 184 -> 3864, fp32 Y: 22 in place of 16 us).  All as measured when
+    // it was tried; the same cases take 163, 166, 16.6, 45, 53, 208 and 14.2 us now.
     if ((static_cast<int64_t>(a.M) + EX_ROWS - 1) / EX_ROWS * strips >= 148) {
         while (a.depth > 1 && ex_smem(BF, YT, atoms, a.depth) > kTwoDynSmem) --a.depth;
         if (ex_smem(BF, YT, atoms, a.depth) > kTwoDynSmem) {
@@ -1263,6 +1272,13 @@ hq_status launch_few(const ShrinkArgs& s, const ExpandArgs& e, int tiles, cudaSt
 
 template <bool BF, int YT>
 hq_status launch_lora_y(const ShrinkArgs& s, const ExpandArgs& e, int tiles, cudaStream_t st) {
+    // How many tokens a tile holds is known on the GPU only; `tiles` is the plan's bound
+    // M / 64 + min(n + 1, M), which grows with the adapters in memory.  Below 16 tokens for
+    // each of them the few-token form: what decode wants (1 and 16 tokens 5.8 and 9.4 us in
+    // place of 5.9 and 9.6 for two kernels), but also what long prompts get beside many
+    // resident adapters: 1024 tokens of one request, 4096 -> 11008, rank 32, take 26 us
+    // beside 8 adapters and 156 beside 64, 4096 tokens of 12 requests 60 beside 16 and 405
+    // beside 256.
     if (s.M < 16 * tiles && s.r <= 64)
         return s.r <= 16   ? launch_few<BF, YT, 16>(s, e, tiles, st)
                : s.r <= 32 ? launch_few<BF, YT, 32>(s, e, tiles, st)

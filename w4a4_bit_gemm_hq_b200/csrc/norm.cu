@@ -4,7 +4,7 @@
 // rotation and quantiser (kernel K1 without the normed row in between).
 //
 // Per row m of K channels, all in fp32, every product and sum rounded on its
-// own (no fma), e = the 16-bit or fp32 type of the stream:
+// own (no fma but in the sums of squares), e = the 16-bit or fp32 type of the stream:
 //   p = y,  or  fl(fl(y * fl(w_post + off)) * ry)  with the norm after the block
 //   p = fl(gate * p)                               with a gate
 //   h = e(fl(H + fl(alpha * p)))                   (h = H without a block)
@@ -227,11 +227,13 @@ __device__ __forceinline__ float inv_rms(float sum, int K, float eps) {
 // ---------------------------------------------------------- without a quantiser
 // A CTA walks rows m, m + grid, ...; NV vectors per thread, vector i of thread t
 // at i * threads + t.  Bound by HBM (4096 x 4096 bf16 with norms on both sides and a
-// gate per token: 30.7 us, 5.5 TB/s of the 6.55 of a copy; fp32 rows by their
-// wait for memory, with one set of registers: 1537 x 5003 in 28.2 us, 4.4 TB/s): the weights stay in registers as fp32 over
-// the CTA's rows (KEEP) and the next row is requested before this one is worked
-// on; rows whose registers do not allow both (fp32, very wide ones) have the
-// weights in shared memory and request the next row at the end of this one.  A row is in registers from its load to its stores.
+// gate per token: 30.3 us, 5.5 TB/s of the 6.55 of a copy; fp32 rows by their wait
+// for memory, with one set of registers, and by uneven rounds: 1537 x 5003 in 28.3 us,
+// 4.4 TB/s, is 5.2 rows for each of 296 CTAs, so six): the weights stay in registers
+// as fp32 over the CTA's rows (KEEP) and the next row is requested before this one is
+// worked on; rows whose registers do not allow both (fp32, very wide ones) have the
+// weights in shared memory and request the next row at the end of this one.  A row is
+// in registers from its load to its stores.
 template <int XT, int NV, bool POST, bool KEEP, bool TAIL, int MAXT>
 __global__ void __launch_bounds__(MAXT, !KEEP && MAXT == 512 ? 2 : 1) k_residual_norm(const NormArgs a) {
     constexpr int V = vec_len<XT>;
@@ -384,8 +386,9 @@ __global__ void __launch_bounds__(MAXT, !KEEP && MAXT == 512 ? 2 : 1) k_residual
 // 8 (c / 256), which makes the accesses of all layouts free of bank conflicts; the
 // weights lie in slots of 16 bytes that only their lane uses.
 // Measured: 2048 x 4096, group 4096, 8 bits 18.7 us (9.0 at HBM's rate); 8192 x 8192,
-// group 256, 4 bits, the normed rows and a gate per channel 116 us (87), per token 126
-// (107).  Bound by the latency of its instructions at 16 warps per SM (128 registers):
+// group 256, 4 bits, the normed rows and a gate per channel 116 us (87), per token 125
+// (107); codes only, 8192 x 4096, group 128, 4 bits 35.0 us (12.8) without a block, 43.1
+// (33.3) with one.  Bound by the latency of its instructions at 16 warps per SM (128 registers):
 // about 34 per value, issued at 0.5 per cycle and scheduler.  With fewer registers it
 // spills and is slower; with 16 values per thread and 32 warps per SM the work per row
 // and thread (reductions, divisions, addresses) weighs twice: 20.3 and 160 us.
@@ -479,7 +482,7 @@ __device__ __forceinline__ void stages_d(float (&v)[32], float* base, int t) {
 // FULL: rows of a multiple of 1024 channels, every vector is there.
 // IN: the operands beside H: none, Y, or Y and the gate, whose next row is requested
 // before the codes are written (at its use it cost 180 us in place of 126 at 8192 x
-// 8192).  Without Y the registers allow 20 warps per SM (8192 x 4096, group 128: 35.4 us,
+// 8192).  Without Y the registers allow 20 warps per SM (8192 x 4096, group 128: 35.0 us,
 // 37.8 at 16; rows of more than 10 warps do not gain).
 template <int XT, int BITS, bool FULL, int IN>
 __global__ void __launch_bounds__(IN == 0 ? 640 : 512) k_norm_quant(const NormArgs a) {
